@@ -420,6 +420,107 @@ MX_API int mx_gemm_quantize_x4(const void *a_codes, const void *a_scales, mx_fmt
                                mx_fmt out_fmt, mx_round out_rnd, uint64_t out_seed,
                                void *out_codes, void *out_scales, mx_scale_layout out_sl, void *stream);
 
+/*
+ * mx_rmsnorm, mx_rmsnorm_quantize -- RMS norm of each row, with an optional
+ * residual addition in front of it; the second form casts the result along
+ * its rows (Algorithm 1 of section 3), the layout a block-scaled GEMM reads as
+ * its operand, without writing the normalised tensor first (the principle of a
+ * producer that writes what its consumer reads, "Format-Aware Fusion for Fast
+ * FP4 Pretraining", abstract).  Per row:
+ *    h    = x + residual, rounded to xdt (with a residual; else h = x)
+ *    rstd = 1 / sqrt(sum_c h_c^2 / cols + eps)
+ *    y_c  = (h_c * rstd) * weight_c
+ * The sum of squares is fp32 in an order fixed by cols and xdt; every other
+ * step is one IEEE fp32 operation.  The squares overflow fp32 for |h| above
+ * 1.8e19: rstd is then 0.  A NaN in h makes its whole row of y NaN; an Inf
+ * makes rstd 0, and y is NaN at the Inf and zero elsewhere.
+ *
+ *  x        device, rows x cols, ldx elements per row, type xdt; 16-byte
+ *           aligned, ldx * sizeof(elem) a multiple of 16; the same holds for
+ *           residual, h and y, all of type xdt.
+ *  residual NULL, or a tensor of x's shape; then h is required, and NULL
+ *           without it.  h receives the sum and may be x or residual itself.
+ *  weight   device, cols values of type wdt, 16-byte aligned.
+ *  eps      finite, not negative.
+ *  y        the normalised values rounded to xdt: required by mx_rmsnorm,
+ *           optional (NULL) in mx_rmsnorm_quantize.  May be x itself.
+ *  rstd     NULL, or device, rows fp32 values (for the backward pass).
+ *  fmt, rnd, seed, codes, scales, sl  as for mx_quantize with block_axis 1 on
+ *           the fp32 y (before its rounding to xdt): the same bytes, the
+ *           stochastic-rounding positions included.  Padding bytes of the
+ *           scale layouts are not written.
+ *  cols     a multiple of 32 (MX_ERR_SHAPE), at most 32768; rows at most
+ *           2^31 - 1 (MX_ERR_UNSUPPORTED).
+ * Errors: MX_ERR_ARG, MX_ERR_ALIGN, MX_ERR_SHAPE, MX_ERR_UNSUPPORTED,
+ * MX_ERR_SR_RANGE, MX_ERR_CUDA.
+ */
+MX_API int mx_rmsnorm(const void *x, mx_dtype xdt, int64_t rows, int64_t cols, int64_t ldx, const void *residual,
+                      int64_t ldr, const void *weight, mx_dtype wdt, float eps, void *h, int64_t ldh, void *y,
+                      int64_t ldy, float *rstd, void *stream);
+MX_API int mx_rmsnorm_quantize(const void *x, mx_dtype xdt, int64_t rows, int64_t cols, int64_t ldx,
+                               const void *residual, int64_t ldr, const void *weight, mx_dtype wdt, float eps,
+                               mx_fmt fmt, mx_round rnd, uint64_t seed, void *h, int64_t ldh, void *y, int64_t ldy,
+                               float *rstd, void *codes, void *scales, mx_scale_layout sl, void *stream);
+
+/*
+ * mx_rmsnorm_backward -- the gradients of mx_rmsnorm with respect to h and the
+ * weight.  With n = h * rstd and a = dy * weight, per row
+ *    dx = rstd * (a - n * (sum_c a_c n_c) / cols) + dres     (dres as 0 if NULL)
+ * rounded to xdt, the gradient of x and of the residual alike when dres is the
+ * gradient that reaches h by its other uses; and dweight_c = sum over the rows
+ * of dy * n.  All sums are fp32, in an order fixed by the sizes and types.  The
+ * gradient of a cast result is taken as that of y.
+ *
+ *  dy, h, dres, dx  device, rows x cols, type xdt, aligned as in mx_rmsnorm;
+ *           h and rstd as mx_rmsnorm wrote or read them.  dx may be dy or dres.
+ *  dweight  device, cols fp32 values; overwritten.  Zero for rows = 0.
+ *  workspace  device, mx_rmsnorm_backward_workspace_bytes(rows, cols) bytes,
+ *           16-byte aligned, used by one call at a time.
+ * Limits and errors as for mx_rmsnorm; MX_ERR_ARG if ws_bytes is too small.
+ */
+MX_API int mx_rmsnorm_backward(const void *dy, mx_dtype xdt, int64_t rows, int64_t cols, int64_t lddy,
+                               const void *h, int64_t ldh, const void *weight, mx_dtype wdt, const float *rstd,
+                               const void *dres, int64_t lddres, void *dx, int64_t lddx, float *dweight,
+                               void *workspace, size_t ws_bytes, void *stream);
+MX_API size_t mx_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * mx_gemv, mx_gemv_nvfp4 -- y = alpha * x W^T for a few tokens (rows of x),
+ * the weights in MXFP4 or NVFP4 and the activations as they are (section 4's
+ * compute flow with one quantized operand: decoding reads every weight once
+ * for each handful of tokens, and four bits of it).  The weights' buffers are
+ * those of mx_gemm's and mx_gemm_nvfp4's B operand, so that one copy of the
+ * weights serves both.  Products with the codes are exact, sums are fp32 in an
+ * order fixed by N, K, the layout and the types, whatever the other tokens
+ * are; the scales multiply fp32 partial sums (MXFP4) or enter exactly
+ * (NVFP4: 2^8-scaled inside), and the result is rounded once to ydt.
+ *
+ *  w_codes  device, N x K codes (K / 2 bytes per row), 16-byte aligned.
+ *  fw       MX_E2M1 (MX_ERR_UNSUPPORTED for the other formats).
+ *  w_scales device, mx_scales_bytes(sl, N, K) bytes, respectively
+ *           mx_nvfp4_scales_bytes(sl, N, K); 16-byte aligned in the MMA
+ *           layouts.  Any layout; padding bytes are not used.
+ *  w_enc, w_domain_rows  NVFP4: the encode scales and rows per domain, as
+ *           mx_quantize_nvfp4 took and wrote them (any number of rows).
+ *  x        device, M x K, ldx elements per row, type xdt; 16-byte aligned,
+ *           ldx * sizeof(elem) a multiple of 16.
+ *  y        device, M x N, ldy elements per row, type ydt.
+ *  K        a multiple of 32 (MXFP4) or 16 (NVFP4), else MX_ERR_SHAPE; K = 0
+ *           gives zeros.  M at most 65536, N and K at most 2^31 - 1, scales
+ *           below 4 GiB (MX_ERR_UNSUPPORTED).  Any M is right; mx_gemm is the
+ *           faster call from a few dozen tokens on.
+ * A NaN scale makes its block's products NaN; NaN and Inf in x go by IEEE
+ * rules (0 * Inf is NaN).
+ * Errors: MX_ERR_ARG, MX_ERR_ALIGN, MX_ERR_SHAPE, MX_ERR_UNSUPPORTED,
+ * MX_ERR_CUDA.
+ */
+MX_API int mx_gemv(const void *w_codes, const void *w_scales, mx_fmt fw, mx_scale_layout sl, const void *x,
+                   mx_dtype xdt, int64_t ldx, int64_t M, int64_t N, int64_t K, float alpha, void *y, mx_dtype ydt,
+                   int64_t ldy, void *stream);
+MX_API int mx_gemv_nvfp4(const void *w_codes, const void *w_scales, const float *w_enc, int64_t w_domain_rows,
+                         mx_scale_layout sl, const void *x, mx_dtype xdt, int64_t ldx, int64_t M, int64_t N,
+                         int64_t K, float alpha, void *y, mx_dtype ydt, int64_t ldy, void *stream);
+
 /* Byte sizes of the buffers above (0 for invalid arguments). */
 MX_API size_t mx_codes_bytes(mx_fmt fmt, int64_t outer, int64_t inner);
 MX_API size_t mx_scales_bytes(mx_scale_layout sl, int64_t outer, int64_t inner);
@@ -430,7 +531,7 @@ MX_API size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * MX_ERR_TIMEOUT if a kernel gave up a bounded wait since the last call.
  * MX_ERR_CUDA if the synchronisation itself failed.  In the debug build
  * (libmx_debug.so, compiled with MX_DEBUG) every code and scale store of the
- * casts and the NVFP4 cast, and every code and scale load of the decode,
+ * casts, the NVFP4 cast and the norm's cast, and every code and scale load of the decode,
  * checks its byte range against its buffer's size first; a range
  * outside the buffer is skipped and reported here as MX_ERR_BOUNDS (after a
  * timeout, which takes precedence).  The release build has no such checks. */

@@ -1,7 +1,7 @@
 """Build libmx.so (the C-ABI library) in-tree with nvcc for sm_100a, and on
 request libmx_debug.so: the same sources compiled with MX_DEBUG, whose cast
-kernels (MX, dual and NVFP4) check every code and scale store, and the
-decode its loads, against the buffer sizes, and report a range outside a
+kernels (MX, dual, NVFP4 and the norm's) check every code and scale store, and
+the decode its loads, against the buffer sizes, and report a range outside a
 buffer as MX_ERR_BOUNDS instead of touching it.
 
 Usage: python -m microscaling_block_scaled_mx_b200.build [--force] [--debug]
@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmx.so")
 DEBUG_LIB = os.path.join(PKG, "libmx_debug.so")
-SOURCES = ["mx_api.cu", "mx_cast.cu", "mx_gemm.cu", "mx_nvfp4.cu"]
+SOURCES = ["mx_api.cu", "mx_cast.cu", "mx_gemm.cu", "mx_nvfp4.cu", "mx_norm.cu", "mx_gemv.cu"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",

@@ -504,14 +504,196 @@ int mx_gemm_nvfp4_x4(const void *a_codes, const void *a_scales, const float *a_e
                            K, alpha, c, cdt, ldc, true, stream);
 }
 
+}  // extern "C"
+
+namespace {
+
+// The size limits of the norm kernels: a row lives in one CTA's registers.
+constexpr int64_t kNormMaxCols = 32768;
+constexpr int64_t kMaxGrid = 2147483647;
+
+// CTAs of the backward pass, each with one row of partial sums of dweight:
+// four for each of the 148 SMs, whatever the device, so that the workspace's
+// size and the order of the sums depend on the sizes alone.
+int64_t norm_parts(int64_t rows) { return rows < 592 ? rows : 592; }
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// A matrix of `cols` values of type dt per row: MX_OK, or what is wrong.
+int check_matrix(const void *p, int dt, int64_t cols, int64_t ld) {
+    if (!p || ld < cols) return MX_ERR_ARG;
+    return aligned16(p) && (ld % 8) * dtype_bytes(dt) % 16 == 0 ? MX_OK : MX_ERR_ALIGN;
+}
+
+struct MatrixArg {
+    const void *p;
+    int64_t ld;
+    bool optional;
+};
+
+// The worst of several matrices: MX_ERR_ARG before MX_ERR_ALIGN.
+template <int N>
+int check_matrices(const MatrixArg (&m)[N], int dt, int64_t cols) {
+    int rc = MX_OK;
+    for (const MatrixArg &a : m) {
+        if (a.optional && !a.p) continue;
+        const int r = check_matrix(a.p, dt, cols, a.ld);
+        if (r == MX_ERR_ARG) return r;
+        if (r != MX_OK) rc = r;
+    }
+    return rc;
+}
+
+int rmsnorm_impl(const void *x, mx_dtype xdt, int64_t rows, int64_t cols, int64_t ldx, const void *residual,
+                 int64_t ldr, const void *weight, mx_dtype wdt, float eps, bool cast, mx_fmt fmt, mx_round rnd,
+                 uint64_t seed, void *h, int64_t ldh, void *y, int64_t ldy, float *rstd, void *codes, void *scales,
+                 mx_scale_layout sl, void *stream) {
+    if ((xdt != MX_F32 && xdt != MX_BF16) || (wdt != MX_F32 && wdt != MX_BF16)) return MX_ERR_ARG;
+    if (cast && (elem_bits(fmt) == 0 || (rnd != MX_RNE && rnd != MX_SR) || !valid_layout(sl))) return MX_ERR_ARG;
+    if (rows < 0 || cols < 0 || !(eps >= 0.0f && eps <= 3.4028234663852886e38f)) return MX_ERR_ARG;
+    if (cols % 32 != 0) return MX_ERR_SHAPE;
+    if (rows == 0 || cols == 0) return MX_OK;             // empty: pointers may be NULL
+    if (!weight || (residual == nullptr) != (h == nullptr)) return MX_ERR_ARG;
+    if (cast ? (!codes || !scales) : !y) return MX_ERR_ARG;
+    const MatrixArg m[4] = {{x, ldx, false}, {residual, ldr, true}, {h, ldh, true}, {y, ldy, true}};
+    const int rc = check_matrices(m, xdt, cols);
+    if (rc != MX_OK) return rc;
+    if (!aligned16(weight) || (rstd && !aligned4(rstd)) || (cast && !aligned16(codes))) return MX_ERR_ALIGN;
+    if (cols > kNormMaxCols || rows > kMaxGrid) return MX_ERR_UNSUPPORTED;
+    if (cast && rnd == MX_SR && static_cast<uint64_t>(rows) * static_cast<uint64_t>(cols) > (1ull << 34))
+        return MX_ERR_SR_RANGE;
+    if (cast && mx_scales_bytes(sl, rows, cols) >= (1ull << 32)) return MX_ERR_UNSUPPORTED;
+    MxNormArgs a;
+    a.x = x; a.residual = residual; a.xdt = xdt; a.rows = rows; a.cols = cols; a.ldx = ldx; a.ldr = ldr;
+    a.weight = weight; a.wdt = wdt; a.eps = eps; a.h = h; a.y = y; a.ldh = ldh; a.ldy = ldy; a.rstd = rstd;
+    a.fmt = fmt; a.rnd = rnd; a.seed = seed; a.codes = cast ? codes : nullptr; a.scales = scales; a.sl = sl;
+    a.num_sms = sm_count(nullptr);
+    if (a.num_sms <= 0) return MX_ERR_CUDA;
+    return mx_launch_rmsnorm(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mx_rmsnorm(const void *x, mx_dtype xdt, int64_t rows, int64_t cols, int64_t ldx, const void *residual,
+               int64_t ldr, const void *weight, mx_dtype wdt, float eps, void *h, int64_t ldh, void *y, int64_t ldy,
+               float *rstd, void *stream) {
+    const NvtxRange nvtx_range("mx_rmsnorm");
+    return rmsnorm_impl(x, xdt, rows, cols, ldx, residual, ldr, weight, wdt, eps, false, MX_E4M3, MX_RNE, 0, h, ldh,
+                        y, ldy, rstd, nullptr, nullptr, MX_SCALES_PLAIN, stream);
+}
+
+int mx_rmsnorm_quantize(const void *x, mx_dtype xdt, int64_t rows, int64_t cols, int64_t ldx, const void *residual,
+                        int64_t ldr, const void *weight, mx_dtype wdt, float eps, mx_fmt fmt, mx_round rnd,
+                        uint64_t seed, void *h, int64_t ldh, void *y, int64_t ldy, float *rstd, void *codes,
+                        void *scales, mx_scale_layout sl, void *stream) {
+    const NvtxRange nvtx_range("mx_rmsnorm_quantize");
+    return rmsnorm_impl(x, xdt, rows, cols, ldx, residual, ldr, weight, wdt, eps, true, fmt, rnd, seed, h, ldh, y,
+                        ldy, rstd, codes, scales, sl, stream);
+}
+
+size_t mx_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0 || cols % 32 != 0 || cols > kNormMaxCols) return 0;
+    return static_cast<size_t>(norm_parts(rows)) * static_cast<size_t>(cols) * sizeof(float);
+}
+
+int mx_rmsnorm_backward(const void *dy, mx_dtype xdt, int64_t rows, int64_t cols, int64_t lddy, const void *h,
+                        int64_t ldh, const void *weight, mx_dtype wdt, const float *rstd, const void *dres,
+                        int64_t lddres, void *dx, int64_t lddx, float *dweight, void *workspace, size_t ws_bytes,
+                        void *stream) {
+    const NvtxRange nvtx_range("mx_rmsnorm_backward");
+    if ((xdt != MX_F32 && xdt != MX_BF16) || (wdt != MX_F32 && wdt != MX_BF16)) return MX_ERR_ARG;
+    if (rows < 0 || cols < 0) return MX_ERR_ARG;
+    if (cols % 32 != 0) return MX_ERR_SHAPE;
+    if (cols == 0) return MX_OK;                          // empty: pointers may be NULL
+    if (!dweight) return MX_ERR_ARG;
+    if (!aligned4(dweight)) return MX_ERR_ALIGN;
+    if (cols > kNormMaxCols) return MX_ERR_UNSUPPORTED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (rows == 0)                                        // the sum over no rows
+        return cudaMemsetAsync(dweight, 0, static_cast<size_t>(cols) * 4, st) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+    if (!weight || !rstd || !workspace || ws_bytes < mx_rmsnorm_backward_workspace_bytes(rows, cols))
+        return MX_ERR_ARG;
+    const MatrixArg m[4] = {{dy, lddy, false}, {h, ldh, false}, {dx, lddx, false}, {dres, lddres, true}};
+    const int rc = check_matrices(m, xdt, cols);
+    if (rc != MX_OK) return rc;
+    if (!aligned16(weight) || !aligned4(rstd) || !aligned16(workspace)) return MX_ERR_ALIGN;
+    MxNormBackArgs a;
+    a.dy = dy; a.h = h; a.dres = dres; a.xdt = xdt; a.rows = rows; a.cols = cols;
+    a.lddy = lddy; a.ldh = ldh; a.lddres = lddres; a.lddx = lddx; a.weight = weight; a.wdt = wdt; a.rstd = rstd;
+    a.dx = dx; a.dweight = dweight; a.part = static_cast<float *>(workspace); a.parts = norm_parts(rows);
+    a.num_sms = sm_count(nullptr);
+    if (a.num_sms <= 0) return MX_ERR_CUDA;
+    return mx_launch_rmsnorm_backward(a, st) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+int gemv_impl(const void *w_codes, const void *w_scales, mx_scale_layout sl, bool nv, const float *w_enc,
+              int64_t w_domain_rows, const void *x, mx_dtype xdt, int64_t ldx, int64_t M, int64_t N, int64_t K,
+              float alpha, void *y, mx_dtype ydt, int64_t ldy, void *stream) {
+    if ((xdt != MX_F32 && xdt != MX_BF16) || (ydt != MX_F32 && ydt != MX_BF16) || !valid_layout(sl)) return MX_ERR_ARG;
+    if (M < 0 || N < 0 || K < 0 || w_domain_rows < 0) return MX_ERR_ARG;
+    if (K % (nv ? 16 : 32) != 0) return MX_ERR_SHAPE;
+    if (M == 0 || N == 0) return MX_OK;                   // empty: pointers may be NULL
+    if (!y || ldy < N) return MX_ERR_ARG;
+    const size_t esz = static_cast<size_t>(dtype_bytes(ydt));
+    if (reinterpret_cast<uintptr_t>(y) % esz != 0) return MX_ERR_ALIGN;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (K == 0)
+        return cudaMemset2DAsync(y, ldy * esz, 0, N * esz, M, st) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+    if (!w_codes || !w_scales || (nv && !w_enc)) return MX_ERR_ARG;
+    const int rc = check_matrix(x, xdt, K, ldx);
+    if (rc != MX_OK) return rc;
+    if (!aligned16(w_codes) || (sl != MX_SCALES_PLAIN && !aligned16(w_scales)) || (nv && !aligned4(w_enc)))
+        return MX_ERR_ALIGN;
+    constexpr int64_t kMax = 2147483647;
+    if (N > kMax || K > kMax || M > 65536) return MX_ERR_UNSUPPORTED;     // 32-bit indices, the grid's second axis
+    const size_t sbytes = nv ? mx_nvfp4_scales_bytes(sl, N, K) : mx_scales_bytes(sl, N, K);
+    if (sbytes >= (1ull << 32)) return MX_ERR_UNSUPPORTED;                // 32-bit scale offsets
+    MxGemvArgs a;
+    a.codes = w_codes; a.scales = w_scales; a.enc = nv ? w_enc : nullptr;
+    a.lines = w_domain_rows == 0 || w_domain_rows > N ? N : w_domain_rows;
+    a.sl = sl; a.x = x; a.xdt = xdt; a.ldx = ldx; a.M = M; a.N = N; a.K = K; a.alpha = alpha;
+    a.y = y; a.ydt = ydt; a.ldy = ldy;
+    a.num_sms = sm_count(nullptr);
+    if (a.num_sms <= 0) return MX_ERR_CUDA;
+    return mx_launch_gemv(a, st) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mx_gemv(const void *w_codes, const void *w_scales, mx_fmt fw, mx_scale_layout sl, const void *x, mx_dtype xdt,
+            int64_t ldx, int64_t M, int64_t N, int64_t K, float alpha, void *y, mx_dtype ydt, int64_t ldy,
+            void *stream) {
+    const NvtxRange nvtx_range("mx_gemv");
+    if (elem_bits(fw) == 0) return MX_ERR_ARG;
+    if (fw != MX_E2M1) return MX_ERR_UNSUPPORTED;         // 4-bit weights only
+    return gemv_impl(w_codes, w_scales, sl, false, nullptr, 0, x, xdt, ldx, M, N, K, alpha, y, ydt, ldy, stream);
+}
+
+int mx_gemv_nvfp4(const void *w_codes, const void *w_scales, const float *w_enc, int64_t w_domain_rows,
+                  mx_scale_layout sl, const void *x, mx_dtype xdt, int64_t ldx, int64_t M, int64_t N, int64_t K,
+                  float alpha, void *y, mx_dtype ydt, int64_t ldy, void *stream) {
+    const NvtxRange nvtx_range("mx_gemv_nvfp4");
+    return gemv_impl(w_codes, w_scales, sl, true, w_enc, w_domain_rows, x, xdt, ldx, M, N, K, alpha, y, ydt, ldy,
+                     stream);
+}
+
 int mx_last_device_status(void *stream) {
-    // the GEMMs', the casts' and the NVFP4 unit's status words, all read and
-    // cleared; a timeout takes precedence over a debug-build bounds report
+    // the GEMMs', the casts', the NVFP4 unit's and the norm's status words, all
+    // read and cleared; a timeout takes precedence over a debug-build bounds report
     const int g = mx_read_device_status(static_cast<cudaStream_t>(stream));
     const int c = mx_read_cast_status();
     const int n = mx_read_nvfp4_bounds_status();
+    const int r = mx_read_norm_bounds_status();
     if (g == MX_ERR_TIMEOUT || c == MX_ERR_TIMEOUT) return MX_ERR_TIMEOUT;
-    return g != MX_OK ? g : (c != MX_OK ? c : n);
+    return g != MX_OK ? g : (c != MX_OK ? c : (n != MX_OK ? n : r));
 }
 
 }  // extern "C"

@@ -89,6 +89,52 @@ struct MxGemmArgs {
     int device;
 };
 
+struct MxNormArgs {
+    const void *x, *residual;      // residual NULL: h is x
+    int xdt;
+    int64_t rows, cols, ldx, ldr;
+    const void *weight;
+    int wdt;
+    float eps;
+    void *h, *y;                   // y may be NULL when codes is not
+    int64_t ldh, ldy;
+    float *rstd;                   // may be NULL
+    int fmt, rnd;
+    uint64_t seed;
+    void *codes, *scales;          // NULL: no cast
+    int sl;
+    int num_sms;
+};
+
+struct MxNormBackArgs {
+    const void *dy, *h, *dres;     // dres may be NULL
+    int xdt;
+    int64_t rows, cols, lddy, ldh, lddres, lddx;
+    const void *weight;
+    int wdt;
+    const float *rstd;
+    void *dx;
+    float *dweight, *part;         // part: parts x cols partial sums
+    int64_t parts;
+    int num_sms;
+};
+
+struct MxGemvArgs {
+    const void *codes, *scales;
+    const float *enc;              // NVFP4: fp32 encode scales (NULL: MXFP4)
+    int64_t lines;                 // NVFP4: weight rows per encode scale
+    int sl;
+    const void *x;
+    int xdt;
+    int64_t ldx;
+    int64_t M, N, K;
+    float alpha;
+    void *y;
+    int ydt;
+    int64_t ldy;
+    int num_sms;
+};
+
 // MurmurHash3 32-bit finaliser on the host (seed key of stochastic rounding).
 inline uint32_t fmix32_host(uint32_t h) {
     h ^= h >> 16;
@@ -103,6 +149,9 @@ cudaError_t mx_launch_quantize(const MxQuantizeArgs &a, cudaStream_t st);
 cudaError_t mx_launch_quantize_dual(const MxQuantizeDualArgs &a, cudaStream_t st);
 cudaError_t mx_launch_dequantize(const MxDequantArgs &a, cudaStream_t st);
 cudaError_t mx_launch_quantize_nvfp4(const MxNvfp4Args &a, cudaStream_t st);
+cudaError_t mx_launch_rmsnorm(const MxNormArgs &a, cudaStream_t st);
+cudaError_t mx_launch_rmsnorm_backward(const MxNormBackArgs &a, cudaStream_t st);
+cudaError_t mx_launch_gemv(const MxGemvArgs &a, cudaStream_t st);
 // returns an mx_status (MX_OK, MX_ERR_CUDA, MX_ERR_UNSUPPORTED)
 int mx_launch_gemm(const MxGemmArgs &a, cudaStream_t st);
 // reads and clears the device status word of the current device (after a sync)
@@ -111,6 +160,8 @@ int mx_read_device_status(cudaStream_t st);
 int mx_read_cast_status();
 // reads and clears the NVFP4 unit's debug-build bounds word (the caller has synchronised)
 int mx_read_nvfp4_bounds_status();
+// reads and clears the norm unit's debug-build bounds word (the caller has synchronised)
+int mx_read_norm_bounds_status();
 
 namespace mxg {
 // Encodes (or takes from a per-process cache) a 2-D tiled tensor map: d0 x d1

@@ -10,6 +10,7 @@ documented in include/mx.h.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -101,6 +102,22 @@ def lib() -> ctypes.CDLL:
             L.mx_gemm_quantize.restype = i32
             L.mx_gemm_quantize.argtypes = [vp, vp, i32, vp, vp, i32, i64, i64, i64, ctypes.c_float,
                                            i32, i32, u64, vp, vp, i32, vp]
+            L.mx_rmsnorm.restype = i32
+            L.mx_rmsnorm.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, ctypes.c_float, vp, i64, vp, i64,
+                                     vp, vp]
+            L.mx_rmsnorm_quantize.restype = i32
+            L.mx_rmsnorm_quantize.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, ctypes.c_float, i32, i32,
+                                              u64, vp, i64, vp, i64, vp, vp, vp, i32, vp]
+            L.mx_rmsnorm_backward.restype = i32
+            L.mx_rmsnorm_backward.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, vp, vp, i64, vp, i64, vp,
+                                              vp, ctypes.c_size_t, vp]
+            L.mx_rmsnorm_backward_workspace_bytes.restype = ctypes.c_size_t
+            L.mx_rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
+            L.mx_gemv.restype = i32
+            L.mx_gemv.argtypes = [vp, vp, i32, i32, vp, i32, i64, i64, i64, i64, ctypes.c_float, vp, i32, i64, vp]
+            L.mx_gemv_nvfp4.restype = i32
+            L.mx_gemv_nvfp4.argtypes = [vp, vp, vp, i64, i32, vp, i32, i64, i64, i64, i64, ctypes.c_float, vp, i32,
+                                        i64, vp]
             L.mx_codes_bytes.restype = ctypes.c_size_t
             L.mx_codes_bytes.argtypes = [i32, i64, i64]
             L.mx_scales_bytes.restype = ctypes.c_size_t
@@ -346,6 +363,246 @@ def gemm_quantize(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.
                             codes.data_ptr(), scales.data_ptr(), sl, _stream(stream))
     _check(rc, fn)
     return codes, scales
+
+
+def _on(device: int, t: torch.Tensor, what: str) -> torch.Tensor:
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{what} must be on the current CUDA device")
+    return t
+
+
+def _matrix(device: int, t: torch.Tensor, what: str, shape, dtype) -> int:
+    """Check a 2-D row-pitched tensor; returns its leading dimension."""
+    _on(device, t, what)
+    if t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be {shape[0]} x {shape[1]} with unit column stride")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _flat(device: int, t: torch.Tensor, what: str, n: int, dtype) -> torch.Tensor:
+    """Check a contiguous buffer of at least n values."""
+    _on(device, t, what)
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    if t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous and hold {n} values")
+    return t
+
+
+def _here(x: torch.Tensor) -> int:
+    """The index of x's device, which has to be the current one."""
+    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+        raise ValueError("x must be on the current CUDA device")
+    return x.get_device()
+
+
+def _allocating(stream):
+    """New tensors belong to the stream that the call runs on."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _ptr(t) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def _norm_args(x, weight, residual, h, y, want_y, rstd, want_rstd, stream):
+    """Checks and allocations that the norm's two forms share."""
+    if x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError("x must be 2-D with unit column stride")
+    if x.dtype not in DTYPE:
+        raise TypeError("x must be float32 or bfloat16")
+    dev = _here(x)
+    rows, cols = shape = x.shape
+    _on(dev, weight, "weight")
+    if weight.dtype not in DTYPE:
+        raise TypeError("weight must be float32 or bfloat16")
+    if weight.numel() != cols or not weight.is_contiguous():
+        raise ValueError(f"weight must be contiguous and hold {cols} values")
+    if residual is None and h is not None:
+        raise ValueError("h is written only with a residual")
+    new = []
+    if residual is not None and h is None:
+        new.append("h")
+    if want_y and y is None:
+        new.append("y")
+    if want_rstd and rstd is None:
+        new.append("rstd")
+    if new:
+        with _allocating(stream):
+            if "h" in new:
+                h = torch.empty(shape, dtype=x.dtype, device=x.device)
+            if "y" in new:
+                y = torch.empty(shape, dtype=x.dtype, device=x.device)
+            if "rstd" in new:
+                rstd = torch.empty((rows,), dtype=torch.float32, device=x.device)
+    ldx = x.stride(0) if rows > 1 else cols
+    ldr = ldh = ldy = 0
+    if residual is not None:
+        ldr = _matrix(dev, residual, "residual", shape, x.dtype)
+        ldh = _matrix(dev, h, "h", shape, x.dtype)
+    if y is not None:
+        ldy = _matrix(dev, y, "y", shape, x.dtype)
+    if rstd is not None:
+        _flat(dev, rstd, "rstd", rows, torch.float32)
+    return dev, rows, cols, ldx, ldr, h, ldh, y, ldy, rstd
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,
+            with_rstd: bool = False, out=None, stream=None):
+    """RMS norm of each row of a 2-D CUDA tensor (mx_rmsnorm), after adding
+    `residual` to it if one is given.
+
+    Returns (y, h, rstd): y in x's type, h = x + residual (None without a
+    residual), rstd the rows' 1 / sqrt(mean square + eps) as fp32 (None unless
+    asked for).  `out` may supply the three; h may be x or the residual itself
+    and y may be x."""
+    y, h, rstd = out if out is not None else (None, None, None)
+    _, rows, cols, ldx, ldr, h, ldh, y, ldy, rstd = _norm_args(x, weight, residual, h, y, True, rstd, with_rstd,
+                                                               stream)
+    rc = lib().mx_rmsnorm(x.data_ptr(), DTYPE[x.dtype], rows, cols, ldx, _ptr(residual), ldr, weight.data_ptr(),
+                          DTYPE[weight.dtype], eps, _ptr(h), ldh, y.data_ptr(), ldy, _ptr(rstd), _stream(stream))
+    _check(rc, "mx_rmsnorm")
+    return y, h, rstd
+
+
+def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
+                     residual: torch.Tensor | None = None, fmt="e4m3", rnd="rne", seed: int = 0,
+                     scale_layout="mma", with_y: bool = False, with_rstd: bool = False, out=None, stream=None):
+    """The RMS norm of rmsnorm, cast along its rows (mx_rmsnorm_quantize).
+
+    Returns (codes, scales, h, y, rstd): the codes and scales of
+    quantize(y, 1, fmt, ...) on the fp32 y; h, y and rstd as in rmsnorm, each
+    None unless there is a residual, with_y, with_rstd.  `out` may supply the
+    five (None for one that is not wanted or is to be allocated)."""
+    codes, scales, h, y, rstd = out if out is not None else (None,) * 5
+    dev, rows, cols, ldx, ldr, h, ldh, y, ldy, rstd = _norm_args(x, weight, residual, h, y, with_y, rstd, with_rstd,
+                                                                 stream)
+    f, sl = _fmt(fmt), _layout(scale_layout)
+    L = lib()
+    n_codes, n_scales = L.mx_codes_bytes(f, rows, cols), L.mx_scales_bytes(sl, rows, cols)
+    if codes is None or scales is None:
+        with _allocating(stream):
+            if codes is None:
+                codes = torch.empty((rows, codes_row_bytes(f, cols)), dtype=torch.uint8, device=x.device)
+            if scales is None:
+                scales = torch.empty(max(n_scales, 1), dtype=torch.uint8, device=x.device)
+    _flat(dev, codes, "codes", n_codes, torch.uint8)
+    _flat(dev, scales, "scales", n_scales, torch.uint8)
+    rc = L.mx_rmsnorm_quantize(x.data_ptr(), DTYPE[x.dtype], rows, cols, ldx, _ptr(residual), ldr,
+                               weight.data_ptr(), DTYPE[weight.dtype], eps, f,
+                               ROUND[rnd] if isinstance(rnd, str) else int(rnd), seed & (2**64 - 1), _ptr(h), ldh,
+                               _ptr(y), ldy, _ptr(rstd), codes.data_ptr(), scales.data_ptr(), sl, _stream(stream))
+    _check(rc, "mx_rmsnorm_quantize")
+    return codes, scales, h, y, rstd
+
+
+def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                     dres: torch.Tensor | None = None, out=None, workspace: torch.Tensor | None = None,
+                     stream=None):
+    """Gradients of rmsnorm (mx_rmsnorm_backward): h and rstd as the forward
+    pass returned them (h = x without a residual), dres the gradient that
+    reaches h by its other uses.
+
+    Returns (dx, dweight): dx in dy's type, the gradient of x and of the
+    residual, and dweight as fp32.  `out` may supply both (dx may be dy or
+    dres), `workspace` the uint8 scratch of rmsnorm_backward_workspace, which
+    one call at a time may use."""
+    if dy.dim() != 2 or dy.stride(1) != 1:
+        raise ValueError("dy must be 2-D with unit column stride")
+    if dy.dtype not in DTYPE:
+        raise TypeError("dy must be float32 or bfloat16")
+    dev = _here(dy)
+    rows, cols = shape = dy.shape
+    dx, dweight = out if out is not None else (None, None)
+    L = lib()
+    n_ws = L.mx_rmsnorm_backward_workspace_bytes(rows, cols)
+    with _allocating(stream):
+        if dx is None:
+            dx = torch.empty(shape, dtype=dy.dtype, device=dy.device)
+        if dweight is None:
+            dweight = torch.empty((cols,), dtype=torch.float32, device=dy.device)
+        if workspace is None:
+            workspace = torch.empty(max(n_ws, 1), dtype=torch.uint8, device=dy.device)
+    lddy = dy.stride(0) if rows > 1 else cols
+    ldh = _matrix(dev, h, "h", shape, dy.dtype)
+    lddx = _matrix(dev, dx, "dx", shape, dy.dtype)
+    lddres = _matrix(dev, dres, "dres", shape, dy.dtype) if dres is not None else 0
+    _on(dev, weight, "weight")
+    if weight.dtype not in DTYPE:
+        raise TypeError("weight must be float32 or bfloat16")
+    if weight.numel() != cols or not weight.is_contiguous():
+        raise ValueError(f"weight must be contiguous and hold {cols} values")
+    _flat(dev, rstd, "rstd", rows, torch.float32)
+    _flat(dev, dweight, "dweight", cols, torch.float32)
+    _flat(dev, workspace, "workspace", n_ws, torch.uint8)
+    rc = L.mx_rmsnorm_backward(dy.data_ptr(), DTYPE[dy.dtype], rows, cols, lddy, h.data_ptr(), ldh,
+                               weight.data_ptr(), DTYPE[weight.dtype], rstd.data_ptr(), _ptr(dres), lddres,
+                               dx.data_ptr(), lddx, dweight.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                               _stream(stream))
+    _check(rc, "mx_rmsnorm_backward")
+    return dx, dweight
+
+
+def rmsnorm_backward_workspace(rows: int, cols: int, device=None) -> torch.Tensor:
+    """Scratch for rmsnorm_backward on rows x cols."""
+    n = lib().mx_rmsnorm_backward_workspace_bytes(rows, cols)
+    return torch.empty(max(n, 1), dtype=torch.uint8, device="cuda" if device is None else device)
+
+
+def _gemv_args(x, N, K, out_dtype, out, stream):
+    """Checks and allocations that the two weight formats share."""
+    if x.dim() != 2 or x.shape[1] != K or (K > 1 and x.stride(1) != 1):
+        raise ValueError("x must be 2-D, K columns with unit stride")
+    if x.dtype not in DTYPE:
+        raise TypeError("x must be float32 or bfloat16")
+    dev = _here(x)
+    M = x.shape[0]
+    if out is None:
+        with _allocating(stream):
+            out = torch.empty((M, N), dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+    if out.dtype not in DTYPE:
+        raise TypeError("the output must be float32 or bfloat16")
+    ldy = _matrix(dev, out, "out", (M, N), out.dtype)
+    return dev, M, x.stride(0) if M > 1 else K, out, ldy
+
+
+def gemv(w_codes: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, N: int, K: int, fmt="e2m1",
+         alpha: float = 1.0, out_dtype=None, out: torch.Tensor | None = None, scale_layout="mma",
+         stream=None) -> torch.Tensor:
+    """y = alpha * x W^T for the few tokens of x (M x K, not quantized) and N x K
+    MXFP4 weights (mx_gemv): the (codes, scales) quantize returns for W along K
+    in `scale_layout`, the buffers gemm takes as its B operand.  The output has
+    x's type unless out_dtype or `out` says otherwise."""
+    f, sl = _fmt(fmt), _layout(scale_layout)
+    dev, M, ldx, out, ldy = _gemv_args(x, N, K, out_dtype, out, stream)
+    L = lib()
+    _flat(dev, w_codes, "w_codes", L.mx_codes_bytes(f, N, K), torch.uint8)
+    _flat(dev, w_scales, "w_scales", L.mx_scales_bytes(sl, N, K), torch.uint8)
+    rc = L.mx_gemv(w_codes.data_ptr(), w_scales.data_ptr(), f, sl, x.data_ptr(), DTYPE[x.dtype], ldx, M, N, K,
+                   alpha, out.data_ptr(), DTYPE[out.dtype], ldy, _stream(stream))
+    _check(rc, "mx_gemv")
+    return out
+
+
+def gemv_nvfp4(w, x: torch.Tensor, N: int, K: int, domain_rows: int = 0, alpha: float = 1.0, out_dtype=None,
+               out: torch.Tensor | None = None, scale_layout="mma", stream=None) -> torch.Tensor:
+    """gemv with NVFP4 weights (mx_gemv_nvfp4): w is the (codes, scales,
+    enc_scales) triple quantize_nvfp4 returns for W with `domain_rows` in
+    `scale_layout`."""
+    codes, scales, enc = w
+    sl = _layout(scale_layout)
+    dev, M, ldx, out, ldy = _gemv_args(x, N, K, out_dtype, out, stream)
+    L = lib()
+    _flat(dev, codes, "codes", N * K // 2, torch.uint8)
+    _flat(dev, scales, "scales", L.mx_nvfp4_scales_bytes(sl, N, K), torch.uint8)
+    _flat(dev, enc, "enc_scales", L.mx_nvfp4_domains(N, domain_rows), torch.float32)
+    rc = L.mx_gemv_nvfp4(codes.data_ptr(), scales.data_ptr(), enc.data_ptr(), domain_rows, sl, x.data_ptr(),
+                         DTYPE[x.dtype], ldx, M, N, K, alpha, out.data_ptr(), DTYPE[out.dtype], ldy,
+                         _stream(stream))
+    _check(rc, "mx_gemv_nvfp4")
+    return out
 
 
 def last_device_status(stream=None) -> int:
