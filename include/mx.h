@@ -506,8 +506,8 @@ MX_API size_t mx_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
  *           ldx * sizeof(elem) a multiple of 16.
  *  y        device, M x N, ldy elements per row, type ydt.
  *  K        a multiple of 32 (MXFP4) or 16 (NVFP4), else MX_ERR_SHAPE; K = 0
- *           gives zeros.  M at most 65536, N and K at most 2^31 - 1, scales
- *           below 4 GiB (MX_ERR_UNSUPPORTED).  Any M is right; mx_gemm is the
+ *           gives zeros.  M at most 65536, N at most 2^31 - 1, K at most 2^24,
+ *           scales below 4 GiB (MX_ERR_UNSUPPORTED).  Any M is right; mx_gemm is the
  *           faster call from a few dozen tokens on.
  * A NaN scale makes its block's products NaN; NaN and Inf in x go by IEEE
  * rules (0 * Inf is NaN).

@@ -651,7 +651,8 @@ int gemv_impl(const void *w_codes, const void *w_scales, mx_scale_layout sl, boo
     if (!aligned16(w_codes) || (sl != MX_SCALES_PLAIN && !aligned16(w_scales)) || (nv && !aligned4(w_enc)))
         return MX_ERR_ALIGN;
     constexpr int64_t kMax = 2147483647;
-    if (N > kMax || K > kMax || M > 65536) return MX_ERR_UNSUPPORTED;     // 32-bit indices, the grid's second axis
+    // 32-bit indices, 32-bit offsets inside 128 rows of codes, the grid's second axis
+    if (N > kMax || K > (1 << 24) || M > 65536) return MX_ERR_UNSUPPORTED;
     const size_t sbytes = nv ? mx_nvfp4_scales_bytes(sl, N, K) : mx_scales_bytes(sl, N, K);
     if (sbytes >= (1ull << 32)) return MX_ERR_UNSUPPORTED;                // 32-bit scale offsets
     MxGemvArgs a;

@@ -3,15 +3,18 @@
 // E4M3 scale per 16 and an fp32 encode scale per domain of rows), x in bf16 or
 // fp32 as it is.  The weights' buffers are the block-scaled GEMM's operands.
 //
-// A CTA of eight warps takes 128 weight rows (a scale atom's rows) and walks
-// along K in slices of 256 codes: 128 bytes of each row, copied
-// asynchronously into a ring of slices.  A warp multiplies 16 of the rows with
-// eight tokens at a time by m16n8k16 tensor-core products with fp32 sums, a
-// 32-code chunk per pair of products; the chunk's sum times its scale is added
-// to the running sum in fp32.  All operands of the products are exact:
+// The weight rows are cut into tiles of 16 and the tiles dealt out evenly, one
+// CTA per SM; inside a CTA a warp takes a tile, or a part of K of a tile where
+// there are fewer tiles than warps (the parts' sums are added in order through
+// shared memory).  A warp walks along its K in slices of 256 codes, 128 bytes
+// of each row, copied asynchronously into its own ring, so that warps wait for
+// one another only where activations are staged.  It multiplies its 16 rows
+// with eight tokens at a time by m16n8k16 tensor-core products with fp32 sums,
+// a 32-code chunk per pair of products; the chunk's sum times its scale is
+// added to the running sum in fp32.  All operands of the products are exact:
 //  - E2M1 codes become fp16 by the hardware conversion, two per instruction.
 //    NVFP4's E4M3 scale multiplies them there: a code times a scale is a
-//    multiple of 2^-10 below 2688 with six significant bits.
+//    multiple of 2^-10 up to 2688 with six significant bits.
 //  - bf16 activations, times 2^6, are exact in fp16 from 2^-23 up to 2^10.  A
 //    token with a value outside in a slice keeps that slice in bf16, and the
 //    slice is then multiplied in bf16 (the weights, and the other tokens,
@@ -19,13 +22,10 @@
 //  - fp32 activations are split into three bf16 terms (8 + 8 + 8 bits, by
 //    truncation, exact down to bf16's smallest subnormal) whose products go
 //    into the same sum.
-// The CTAs of a cluster split K and add their sums through distributed shared
-// memory in the order of their ranks.  The split depends on N and K alone, and
-// a token is a column of its own, so a token's result does not depend on the
-// other tokens.
-#include <cooperative_groups.h>
+// The split of the work depends on N and K alone, and a token is a column of
+// its own, so a token's result does not depend on the other tokens.
 #include <cstdint>
-#include <cstdlib>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -36,51 +36,62 @@
 namespace mxgemv {
 
 using namespace mxk;
-namespace cg = cooperative_groups;
 
-constexpr int ROWS = 128;            // weight rows per CTA
-constexpr int THREADS = 256;
+constexpr int ATOM = 128;            // weight rows of a scale atom: eight tiles
 constexpr int SLICE = 256;           // codes of a row per slice
-constexpr int DEPTH = 3;             // slices in the ring
+constexpr int DEPTH = 2;             // slices in a warp's ring
 constexpr int PITCH = SLICE / 2 + 16;      // bytes of a row's slice in the ring: eight rows' words in different banks
-constexpr int CODE_BYTES = ROWS * PITCH;
+constexpr int MAX_WARPS = 32;
+constexpr int SMEM_MAX = 227 * 1024;
 
 struct GemvParams {
     const uint8_t *codes, *scales;
     const float *enc;          // NVFP4 encode scales, one per `lines` weight rows
     int64_t lines;
     int sl;
-    bool words;                // plain scales: rows of whole aligned words
+    bool words;                // every scale word is whole and aligned (plain scales may not be)
+    uint32_t full;             // slices that are whole, in 16-byte pieces of codes and scale words
     const void *x;
     int64_t ldx;
     uint32_t tokens, n, k;
+    uint32_t tile;             // tokens of a CTA: min(tokens, 8 NT)
     uint32_t k_blocks, k_groups, slices;
+    uint32_t tiles;            // of 16 rows
+    uint32_t lanes, parts;     // a CTA's warps: tiles at a time x parts of K
+    uint32_t passes;           // times `lanes` tiles
+    uint32_t steps;            // slices of a warp: ceil(slices / parts)
+    uint32_t window;           // steps whose activations are staged together
     float alpha;
     void *y;
     int y_f32;
     int64_t ldy;
 };
 
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, uint32_t bytes, std::integral_constant<int, 16>) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 template <int B>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, uint32_t bytes, std::integral_constant<int, B>) {
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+    if (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(B) : "memory");
+}
+// the first `bytes` from src, zeros behind them
+template <int B>
+__device__ __forceinline__ void copy_async_part(uint32_t dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(B) : "memory");
 }
 
-template <bool BF16>
+// 16 x 8 x 16 products; FIRST: the sum starts from zero.
+template <bool BF16, bool FIRST>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    const float z[4] = {FIRST ? 0.0f : c[0], FIRST ? 0.0f : c[1], FIRST ? 0.0f : c[2], FIRST ? 0.0f : c[3]};
     if (BF16)
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+            "{%10, %11, %12, %13};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]));
     else
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+            "{%10, %11, %12, %13};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]));
 }
 
 // The eight codes of a word as fp16 pairs, code 2i in the low half of q[i].
@@ -95,7 +106,6 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-
 __device__ __forceinline__ void unpack_f16(uint32_t h, float &lo, float &hi) {
     asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
         : "=f"(lo), "=f"(hi) : "r"(h));
@@ -114,12 +124,13 @@ __device__ __forceinline__ uint32_t f16_to_bf16(uint32_t h, float f) {
 
 constexpr float ACT_UP = 64.0f, ACT_DOWN = 1.0f / 64.0f;
 
-// Two E8M0 bytes (bits 0..15) as fp32 2^(s - 127), 0xFF NaN; DOWN: times 2^-6
-// (2^-133 is bf16's smallest subnormal, so the packed product is exact).
+// Two E8M0 bytes (a half of the word) as fp32 2^(s - 127), 0xFF NaN; DOWN: times
+// 2^-6 (2^-133 is bf16's smallest subnormal, so the packed product is exact).
 template <bool DOWN>
-__device__ __forceinline__ void e8m0_pair(uint32_t two, float &lo, float &hi) {
+__device__ __forceinline__ void e8m0_pair(uint32_t word, bool high, float &lo, float &hi) {
     uint32_t r;
-    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
+    if (high) asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, b;\n\t}" : "=r"(r) : "r"(word));
+    else asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, a;\n\t}" : "=r"(r) : "r"(word));
     if (DOWN) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(0x3c803c80u));
     lo = __uint_as_float(r << 16);
     hi = __uint_as_float(r & 0xffff0000u);
@@ -133,76 +144,68 @@ __device__ __forceinline__ void e4m3_pair(uint32_t two, uint32_t &lo, uint32_t &
     hi = __byte_perm(r, 0u, 0x3232u);
 }
 
-// Eight consecutive activations of one token, loaded and turned into the B
-// fragments of a chunk (words of two neighbours).
-template <bool XF32> struct Acts {
-    uint4 v[XF32 ? 2 : 1];
-
-    __device__ __forceinline__ void load(const void *x, int64_t off, bool valid) {
+// Eight bf16 activations as fp16 fragment words, times 2^6, if all 256 of the
+// warp's are exact there, else as they are; returns whether they stayed bf16
+// (the same in every lane).
+__device__ __forceinline__ bool stage_bf16(uint8_t *dst, const uint4 &v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t h[4];
+    bool bad = false;
 #pragma unroll
-        for (int i = 0; i < (XF32 ? 2 : 1); ++i) {
-            v[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (valid)
-                v[i] = XF32 ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(x) + off) + i)
-                            : __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + off));
-        }
+    for (int i = 0; i < 4; ++i) {
+        const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
+        float l2, h2;
+        h[i] = pack_f16(lo * ACT_UP, hi * ACT_UP);
+        unpack_f16(h[i], l2, h2);
+        bad |= !(l2 * ACT_DOWN == lo) || !(h2 * ACT_DOWN == hi);
     }
+    bad = __any_sync(0xffffffffu, bad);
+    *reinterpret_cast<uint4 *>(dst) = bad ? v : make_uint4(h[0], h[1], h[2], h[3]);
+    return bad;
+}
 
-    // bf16: fp16 fragments if every value of the warp's 256 is exact there, else
-    // the bf16 words; returns whether they are bf16 (the same in every lane)
-    __device__ __forceinline__ bool store_f16(uint4 *dst) const {
-        const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-        uint32_t h[4];
-        bool bad = false;
+// Eight fp32 activations as bf16 fragment words of their three terms, the
+// smallest first, `plane` bytes apart.
+__device__ __forceinline__ void stage_f32(uint8_t *dst, const uint4 &v0, const uint4 &v1, uint32_t plane) {
+    const uint32_t b[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    uint32_t t[3][8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
-            float l2, h2;
-            h[i] = pack_f16(lo * ACT_UP, hi * ACT_UP);
-            unpack_f16(h[i], l2, h2);
-            bad |= !(l2 * ACT_DOWN == lo) || !(h2 * ACT_DOWN == hi);
-        }
-        bad = __any_sync(0xffffffffu, bad);
-        *dst = bad ? v[0] : make_uint4(h[0], h[1], h[2], h[3]);
-        return bad;
+    for (int i = 0; i < 8; ++i) {
+        const bool special = (b[i] & 0x7f800000u) == 0x7f800000u;       // Inf or NaN: one term, NaN kept NaN
+        t[2][i] = b[i] & 0xffff0000u;
+        if ((b[i] & 0x7fffffffu) > 0x7f800000u) t[2][i] |= 0x00400000u;
+        const float r = __uint_as_float(b[i]) - __uint_as_float(t[2][i]);
+        t[1][i] = special ? 0u : __float_as_uint(r) & 0xffff0000u;
+        t[0][i] = special ? 0u : __float_as_uint(r - __uint_as_float(t[1][i]));
     }
-
-    // fp32: bf16 fragments of the three terms, the smallest first
-    __device__ __forceinline__ void store_terms(uint4 *dst, int plane_stride) const {
-        const uint32_t b[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[XF32].x, v[XF32].y, v[XF32].z, v[XF32].w};
-        uint32_t t[3][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool special = (b[i] & 0x7f800000u) == 0x7f800000u;       // Inf or NaN: one term, NaN kept NaN
-            t[2][i] = b[i] & 0xffff0000u;
-            if ((b[i] & 0x7fffffffu) > 0x7f800000u) t[2][i] |= 0x00400000u;
-            const float r = __uint_as_float(b[i]) - __uint_as_float(t[2][i]);
-            t[1][i] = special ? 0u : __float_as_uint(r) & 0xffff0000u;
-            t[0][i] = special ? 0u : __float_as_uint(r - __uint_as_float(t[1][i]));
-        }
-#pragma unroll
-        for (int j = 0; j < 3; ++j)
-            dst[j * plane_stride] = make_uint4(__byte_perm(t[j][0], t[j][1], 0x7632u), __byte_perm(t[j][2], t[j][3], 0x7632u),
-                                               __byte_perm(t[j][4], t[j][5], 0x7632u), __byte_perm(t[j][6], t[j][7], 0x7632u));
-    }
-};
+    for (int j = 0; j < 3; ++j)
+        *reinterpret_cast<uint4 *>(dst + j * plane) =
+            make_uint4(__byte_perm(t[j][0], t[j][1], 0x7632u), __byte_perm(t[j][2], t[j][3], 0x7632u),
+                       __byte_perm(t[j][4], t[j][5], 0x7632u), __byte_perm(t[j][6], t[j][7], 0x7632u));
+}
 
 template <bool XF32, bool NV, int NT> struct Shape {
     static constexpr int PLANES = XF32 ? 3 : 1;
     static constexpr int GROUPS = NV ? 4 : 2;                  // scale words of a row per slice
-    static constexpr int SCALE_BYTES = GROUPS * 512;
-    static constexpr int ACT_VECS = NT * PLANES * 256;         // 16-byte fragments of a slice's activations
-    static constexpr int SMEM = DEPTH * (CODE_BYTES + SCALE_BYTES) + 2 * ACT_VECS * 16 + 2 * 8 * NT;
-    static_assert(NT * 8 * ROWS * 4 <= CODE_BYTES, "the sums reuse the ring");
+    static constexpr int SLOT = 16 * PITCH + GROUPS * 64;      // a warp's slice
+    static constexpr int RING = DEPTH * SLOT;                  // of a warp
+    static_assert(NT * 8 * 16 * 4 <= RING, "the sums reuse the ring");
+    // bytes of a token's activations of n slices; the odd 64 put neighbouring tokens in different banks
+    __host__ __device__ static constexpr uint32_t token(uint32_t n) { return n * (SLICE * 2) + 64; }
+    __host__ __device__ static constexpr uint32_t smem(uint32_t warps, uint32_t tile, uint32_t n) {
+        return warps * RING + tile * PLANES * token(n) + n * 8 * NT;
+    }
 };
 
 // The 16 rows x 8 tokens products of the eight chunks of a slice.
 // codes: this lane's word of chunk 0 in its first row; scale: its rows' first
-// scale words.  EXACT16: every token's fragments are fp16, else `bf16` says it
-// of this lane's token of each tile (always, for fp32 activations).
+// scale words; act: its token's fragment of chunk 0, for each tile of tokens.
+// EXACT16: every token's fragments are fp16, else `bf16` says it of this
+// lane's token of each tile (always, for fp32 activations).
 template <bool XF32, bool NV, int NT, bool EXACT16>
-__device__ __forceinline__ void slice_products(const uint8_t *codes, const uint2 *scale, const uint4 *act, uint32_t lane,
-                                               const bool (&bf16)[NT], float (&acc)[NT][4]) {
+__device__ __forceinline__ void slice_products(const uint8_t *codes, uint32_t scale, const uint8_t *const (&act)[NT],
+                                               uint32_t plane, uint32_t lane, const bool (&bf16)[NT], float (&acc)[NT][4]) {
     using S = Shape<XF32, NV, NT>;
     const uint32_t sel = (lane & 2u) ? 0x4431u : 0x4420u;     // NVFP4: this lane's block of chunks c and c + 1
     uint2 words = make_uint2(0u, 0u);
@@ -211,14 +214,15 @@ __device__ __forceinline__ void slice_products(const uint8_t *codes, const uint2
     if (NV && EXACT16) f_lo[0] = f_lo[1] = f_hi[0] = f_hi[1] = ACT_DOWN;
 #pragma unroll(EXACT16 ? 8 : 2)
     for (int c = 0; c < 8; ++c) {
-        if (c % (NV ? 2 : 4) == 0) words = scale[c / (NV ? 2 : 4) * 64];
+        if (c % (NV ? 2 : 4) == 0)
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(words.x), "=r"(words.y) : "r"(scale + c / (NV ? 2 : 4) * 64));
         if (c % 2 == 0) {
             if (NV) {
                 e4m3_pair(__byte_perm(words.x, 0u, sel), m_lo[0], m_lo[1]);
                 e4m3_pair(__byte_perm(words.y, 0u, sel), m_hi[0], m_hi[1]);
             } else {
-                e8m0_pair<EXACT16>(c % 4 == 0 ? words.x & 0xffffu : words.x >> 16, f_lo[0], f_lo[1]);
-                e8m0_pair<EXACT16>(c % 4 == 0 ? words.y & 0xffffu : words.y >> 16, f_hi[0], f_hi[1]);
+                e8m0_pair<EXACT16>(words.x, c % 4 != 0, f_lo[0], f_lo[1]);
+                e8m0_pair<EXACT16>(words.y, c % 4 != 0, f_hi[0], f_hi[1]);
             }
         }
         uint32_t q[4], r[4];
@@ -238,18 +242,19 @@ __device__ __forceinline__ void slice_products(const uint8_t *codes, const uint2
         const uint32_t a0[4] = {q[0], r[0], q[1], r[1]}, a1[4] = {q[2], r[2], q[3], r[3]};
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float part[4];
 #pragma unroll
             for (int j = 0; j < S::PLANES; ++j) {
-                uint4 b = act[(i * S::PLANES + j) * 256 + c * 32];
+                uint4 b = *reinterpret_cast<const uint4 *>(act[i] + j * plane + 64 * c);
                 if (!EXACT16 && !XF32 && !bf16[i]) {
                     b.x = f16_to_bf16(b.x, ACT_DOWN);
                     b.y = f16_to_bf16(b.y, ACT_DOWN);
                     b.z = f16_to_bf16(b.z, ACT_DOWN);
                     b.w = f16_to_bf16(b.w, ACT_DOWN);
                 }
-                mma16816<!EXACT16>(part, a0, b.x, b.y);
-                mma16816<!EXACT16>(part, a1, b.z, b.w);
+                if (j == 0) mma16816<!EXACT16, true>(part, a0, b.x, b.y);
+                else mma16816<!EXACT16, false>(part, a0, b.x, b.y);
+                mma16816<!EXACT16, false>(part, a1, b.z, b.w);
             }
             acc[i][0] = __fmaf_rn(f_lo[c & 1], part[0], acc[i][0]);
             acc[i][1] = __fmaf_rn(f_lo[c & 1], part[1], acc[i][1]);
@@ -259,203 +264,243 @@ __device__ __forceinline__ void slice_products(const uint8_t *codes, const uint2
     }
 }
 
+template <bool NV>
+__device__ __forceinline__ void store_y(const GemvParams &p, uint32_t tok, uint32_t row, float v) {
+    if (tok >= p.tokens || row >= p.n) return;
+    v *= NV ? __fdiv_rn(p.alpha, p.enc[row / p.lines]) : p.alpha;
+    const int64_t off = static_cast<int64_t>(tok) * p.ldy + row;
+    if (p.y_f32) static_cast<float *>(p.y)[off] = v;
+    else static_cast<__nv_bfloat16 *>(p.y)[off] = __float2bfloat16_rn(v);
+}
+
 template <bool XF32, bool NV, int NT>
-__global__ void __launch_bounds__(THREADS) gemv_kernel(const __grid_constant__ GemvParams p) {
+__global__ void __launch_bounds__(32 * MAX_WARPS) gemv_kernel(const __grid_constant__ GemvParams p) {
     using S = Shape<XF32, NV, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t *ring = smem;
-    uint8_t *ring_s = smem + DEPTH * CODE_BYTES;
-    uint4 *acts = reinterpret_cast<uint4 *>(ring_s + DEPTH * S::SCALE_BYTES);
-    uint8_t *flags = reinterpret_cast<uint8_t *>(acts + 2 * S::ACT_VECS);      // [2][8 NT]: the token is in bf16
-
-    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const uint32_t g = lane >> 2, t = lane & 3u;
-    const uint32_t split = cg::this_cluster().num_blocks(), rank = cg::this_cluster().block_rank();
-    const uint32_t row0 = blockIdx.x / split * ROWS;
-    const uint32_t t0 = blockIdx.y * (8 * NT);
-    const uint32_t s_begin = p.slices * rank / split, s_end = p.slices * (rank + 1) / split;
+    const uint32_t win = p.window * p.parts;                   // slices in a window
+    const uint32_t pitch = S::token(win), plane = p.tile * pitch;
+    uint8_t *ring = smem + warp * S::RING;                     // this warp's
+    uint8_t *acts = smem + warps * S::RING;                    // [planes][tile][pitch]
+    uint8_t *flags = acts + S::PLANES * plane;                 // [win][8 NT]: the token is in bf16
+    const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+
+    const uint32_t t0 = blockIdx.y * (8 * NT), count = min(p.tokens - t0, 8u * NT);
+    const uint32_t tile_lo = static_cast<uint32_t>(static_cast<uint64_t>(p.tiles) * blockIdx.x / gridDim.x);
+    const uint32_t tile_hi = static_cast<uint32_t>(static_cast<uint64_t>(p.tiles) * (blockIdx.x + 1) / gridDim.x);
+    const uint32_t col = warp % p.lanes, part = warp / p.lanes;
     const uint32_t row_bytes = p.k / 2;
 
-    // Codes: thread (r, chunk) copies the 16 bytes of rows r, r + 32, r + 64,
-    // r + 96 to the places 16 (r / 4) + r % 4 + {0, 8, 4, 12} of the ring, so
-    // that lane (g, t) of warp w finds its rows at places 16 w + g and + 8.  A
-    // row past the last reads the last one again; its results are not stored.
-    const uint32_t chunk = tid & 7u, r0 = tid >> 3;
-    const uint8_t *src[4];
+    // A tile is the rows 4 w + {0..3} + {0, 32, 64, 96} of a scale atom, a 64-byte
+    // run of each of its 512-byte groups.  Lane (r, chunk) copies 16 bytes of
+    // four rows to the places r + {0, 8, 4, 12} of the slot, so that lane (g, t)
+    // finds its two rows at places g and g + 8.  A row past the last reads the
+    // last one again; its results are not stored.
+    const uint32_t chunk = lane & 7u, r0 = lane >> 3;
+    const uint32_t cdst = ring32 + r0 * PITCH + chunk * 16;
+    // lane l copies scale word l % 16 (of rows r + 32 q: 4 r + q) of group l / 16
+    const uint32_t word = lane & 15u, sgroup = lane >> 4;
+    const uint32_t sstep = p.sl == SL_PLAIN ? 4u : (p.sl == SL_MMA ? 512u : 2048u);     // bytes between groups
+    const uint32_t sdst = ring32 + 16 * PITCH + lane * 4;
+    const uint8_t *codes0;
+    uint32_t src[4], ssrc;          // 32-bit offsets: 128 rows are at most 2^30 bytes, scale buffers below 4 GiB
+    auto set_tile = [&](uint32_t tile) {
+        const uint32_t row0 = tile / 8 * ATOM, w = tile % 8;
+        codes0 = p.codes + static_cast<int64_t>(row0) * row_bytes;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        src[i] = p.codes + static_cast<int64_t>(min(row0 + r0 + 32 * i, p.n - 1)) * row_bytes + chunk * 16;
-    const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-    const uint32_t dst0 = ring32 + ((r0 >> 2) * 16 + (r0 & 3u)) * PITCH + chunk * 16;
-
+        for (int i = 0; i < 4; ++i) src[i] = (min(row0 + 4 * w + r0 + 32 * i, p.n - 1) - row0) * row_bytes + chunk * 16;
+        const uint32_t srow = min(row0 + 4 * w + (word >> 2) + 32 * (word & 3u), p.n - 1);
+        ssrc = (p.sl == SL_PLAIN ? srow * p.k_blocks : tile / 8 * p.k_groups * sstep + 64 * w + 4 * word) + sgroup * sstep;
+    };
     auto issue = [&](uint32_t s, uint32_t slot) {
-        const uint32_t b = s * (SLICE / 2) + chunk * 16;
-        const uint32_t left = b < row_bytes ? row_bytes - b : 0u;
+        const uint32_t at = s * (SLICE / 2);
+        if (s < p.full) {                                      // (uniform) a whole slice of 16-byte pieces and words
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                copy_async<16>(cdst + slot + (8 * (i & 1) + 4 * (i >> 1)) * PITCH, codes0 + (src[i] + at));
+#pragma unroll
+            for (int i = 0; i < S::GROUPS / 2; ++i)
+                copy_async<4>(sdst + slot + i * 128, p.scales + (ssrc + (s * S::GROUPS + 2 * i) * sstep));
+            return;
+        }
+        // the end of K, rows of an odd number of 8-byte blocks, or scale rows off the words
+        const uint32_t b = at + chunk * 16, left = b < row_bytes ? row_bytes - b : 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t to = dst0 + slot * CODE_BYTES + (8 * (i & 1) + 4 * (i >> 1)) * PITCH;
-            const uint8_t *from = left ? src[i] + s * (SLICE / 2) : p.codes;
-            if (!NV || row_bytes % 16 == 0) {
-                copy_async(to, from, left ? 16u : 0u, std::integral_constant<int, 16>{});
-            } else {                                       // rows of an odd number of 8-byte blocks
-                copy_async(to, from, left ? 8u : 0u, std::integral_constant<int, 8>{});
-                copy_async(to + 8, left > 8 ? from + 8 : p.codes, left > 8 ? 8u : 0u, std::integral_constant<int, 8>{});
-            }
+            const uint32_t dst = cdst + slot + (8 * (i & 1) + 4 * (i >> 1)) * PITCH;
+            const uint8_t *from = codes0 + (src[i] + at);
+            copy_async_part<8>(dst, left ? from : p.codes, left ? 8u : 0u);
+            copy_async_part<8>(dst + 8, left > 8 ? from + 8 : p.codes, left > 8 ? 8u : 0u);
         }
-        uint8_t *sdst = ring_s + slot * S::SCALE_BYTES;
-#pragma unroll
-        for (int i = 0; i < S::GROUPS * 128 / THREADS; ++i) {
-            const uint32_t idx = tid + THREADS * i, kg = s * S::GROUPS + (idx >> 7), word = idx & 127u;
+#pragma unroll 1
+        for (int i = 0; i < S::GROUPS / 2; ++i) {
+            const uint32_t kg = s * S::GROUPS + sgroup + 2 * i;
             const uint32_t n = kg * 4 < p.k_blocks ? min(p.k_blocks - kg * 4, 4u) : 0u;   // scales of this word
-            uint8_t *to = sdst + idx * 4;
-            const uint32_t to_s = static_cast<uint32_t>(__cvta_generic_to_shared(to));
-            if (p.sl != SL_PLAIN) {
-                const uint64_t atom = static_cast<uint64_t>(row0 / 128) * p.k_groups + kg;
-                copy_async(to_s, p.scales + (n ? atom * (p.sl == SL_MMA ? 512u : 2048u) + word * 4 : 0u), n,
-                           std::integral_constant<int, 4>{});
+            const uint8_t *from = p.scales + (n ? ssrc + (s * S::GROUPS + 2 * i) * sstep : 0u);
+            if (p.words) {
+                copy_async_part<4>(sdst + slot + i * 128, from, n);
             } else {
-                const uint32_t row = min(row0 + (word >> 2) + 32 * (word & 3u), p.n - 1);
-                const uint8_t *from = p.scales + (n ? static_cast<uint64_t>(row) * p.k_blocks + kg * 4 : 0u);
-                if (p.words) {
-                    copy_async(to_s, from, n, std::integral_constant<int, 4>{});
-                } else {
-                    uint32_t w = 0;
-                    for (uint32_t j = 0; j < n; ++j) w |= static_cast<uint32_t>(__ldg(from + j)) << (8 * j);
-                    *reinterpret_cast<uint32_t *>(to) = w;
-                }
+                uint32_t w = 0;
+                for (uint32_t j = 0; j < n; ++j) w |= static_cast<uint32_t>(__ldg(from + j)) << (8 * j);
+                *reinterpret_cast<uint32_t *>(ring + slot + 16 * PITCH + lane * 4 + i * 128) = w;
             }
         }
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
-    // Activations: warp w takes token w of each tile, lane l the eight values
-    // from 8 l of the slice.  The tokens that are not there stay zero.
-    Acts<XF32> a_next[NT];
-    uint4 *act_mine = acts + (lane >> 2) * 32 + warp * 4 + (lane & 3u);
-    auto has = [&](int i) { return t0 + 8 * i + warp < p.tokens; };
-    auto load_acts = [&](uint32_t s) {
-        const uint32_t col = s * SLICE + lane * 8;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-            if (has(i) && s < s_end)
-                a_next[i].load(p.x, static_cast<int64_t>(t0 + 8 * i + warp) * p.ldx + col, col < p.k);
-    };
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        if (has(i)) continue;
-        for (int b = 0; b < 2; ++b) {
-            for (int j = 0; j < S::PLANES; ++j) act_mine[b * S::ACT_VECS + (i * S::PLANES + j) * 256] = make_uint4(0, 0, 0, 0);
-            if (lane == 0) flags[(b * NT + i) * 8 + warp] = 0;
+    // Activations of the window's slices from s0: a warp takes a (token, slice)
+    // at a time, lane l the eight values from 8 l.
+    auto stage = [&](uint32_t s0) {
+        const uint32_t n = min(win, p.slices - s0);
+        uint32_t tok = warp / n, j = warp % n;
+        while (tok < count) {
+            const uint32_t k = (s0 + j) * SLICE + lane * 8;
+            const int64_t off = static_cast<int64_t>(t0 + tok) * p.ldx + k;
+            uint8_t *dst = acts + tok * pitch + j * (SLICE * 2) + lane * 16;
+            uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+            if (k < p.k) {
+                if (XF32) {
+                    v0 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(p.x) + off));
+                    v1 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(p.x) + off) + 1);
+                } else {
+                    v0 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + off));
+                }
+            }
+            if (XF32) {
+                stage_f32(dst, v0, v1, plane);
+            } else {
+                const bool bad = stage_bf16(dst, v0);
+                if (lane == 0) flags[j * (8 * NT) + tok] = bad;
+            }
+            for (j += warps; j >= n; j -= n) ++tok;
         }
-    }
+    };
+    if (!XF32)
+        for (uint32_t i = threadIdx.x; i < win * 8 * NT; i += blockDim.x)      // the tokens that are not there
+            if (i % (8 * NT) >= count) flags[i] = 0;
 
     float acc[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-
+    const uint8_t *act_mine[NT];            // columns past the last token repeat it; they are not stored
 #pragma unroll
-    for (int i = 0; i < DEPTH - 1; ++i) {
-        if (s_begin + i < s_end) issue(s_begin + i, i);
-        commit();
+    for (int i = 0; i < NT; ++i) act_mine[i] = acts + min(8 * i + g, count - 1) * pitch + t * 16;
+
+    // Step i of a pass is slice i * parts + part of tile pass * lanes + col.
+    uint32_t tile = tile_lo + col, slot = 0;
+    if (tile < tile_hi) {
+        set_tile(tile);
+        if (part < p.slices) issue(part, 0);
     }
-    load_acts(s_begin);
-
-    uint32_t slot = 0;
-    for (uint32_t s = s_begin; s < s_end; ++s) {
-        const uint32_t buf = s & 1u;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            if (!has(i)) continue;
-            uint4 *dst = act_mine + buf * S::ACT_VECS + i * S::PLANES * 256;
-            if (XF32) {
-                a_next[i].store_terms(dst, 256);
-            } else {
-                const bool bad = a_next[i].store_f16(dst);
-                if (lane == 0) flags[(buf * NT + i) * 8 + warp] = bad;
+    commit();
+    for (uint32_t pass = 0; pass < p.passes; ++pass, tile += p.lanes) {
+        uint32_t s = part, s0 = 0, in_window = 0;
+        for (uint32_t i = 0; i < p.steps; ++i, s += p.parts) {
+            if (in_window == 0 && (p.window < p.steps || pass == 0)) {
+                if (i + pass > 0) __syncthreads();             // the last window has been read
+                s0 = i * p.parts;
+                stage(s0);
+                __syncthreads();
             }
-        }
-        asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 2) : "memory");
-        __syncthreads();                                   // slice s is in; slice s - 1 and its activations are free
-        if (s + DEPTH - 1 < s_end) issue(s + DEPTH - 1, slot == 0 ? DEPTH - 1 : slot - 1);
-        commit();
-        load_acts(s + 1);
-
-        const uint8_t *codes = ring + slot * CODE_BYTES + (16 * warp + g) * PITCH + 4 * t;
-        const uint2 *scale = reinterpret_cast<const uint2 *>(ring_s + slot * S::SCALE_BYTES) +
-                             (4 * warp + (g & 3u)) * 2 + (g >> 2);
-        const uint4 *act = acts + buf * S::ACT_VECS + lane;
-        bool bf16[NT];
-        if (XF32) {
-            slice_products<XF32, NV, NT, false>(codes, scale, act, lane, bf16, acc);
-        } else {
-            uint64_t any = 0;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) any |= *reinterpret_cast<const uint64_t *>(flags + (buf * NT + i) * 8);
-            if (any == 0) {
-                slice_products<XF32, NV, NT, !XF32>(codes, scale, act, lane, bf16, acc);
-            } else {
-#pragma unroll
-                for (int i = 0; i < NT; ++i) bf16[i] = flags[(buf * NT + i) * 8 + g];
-                slice_products<XF32, NV, NT, false>(codes, scale, act, lane, bf16, acc);
+            if (++in_window == p.window) in_window = 0;
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncwarp();                   // slice s is in, the other slot free
+            if (i + 1 < p.steps) {
+                if (tile < tile_hi && s + p.parts < p.slices) issue(s + p.parts, S::SLOT - slot);
+            } else if (tile + p.lanes < tile_hi) {
+                set_tile(tile + p.lanes);
+                if (part < p.slices) issue(part, S::SLOT - slot);
             }
+            commit();
+            if (tile < tile_hi && s < p.slices) {
+                const uint8_t *codes = ring + slot + g * PITCH + 4 * t;
+                const uint32_t scale = ring32 + slot + 16 * PITCH + (g & 3u) * 16 + (g >> 2) * 8;
+                const uint8_t *act[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) act[j] = act_mine[j] + (s - s0) * (SLICE * 2);
+                const uint8_t *fl = flags + (s - s0) * (8 * NT);
+                bool bf16[NT];
+                uint64_t any = XF32;
+                if (!XF32) {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) any |= reinterpret_cast<const uint64_t *>(fl)[j];
+                }
+                if (!XF32 && !__any_sync(0xffffffffu, any != 0)) {
+                    slice_products<XF32, NV, NT, !XF32>(codes, scale, act, plane, lane, bf16, acc);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) bf16[j] = XF32 || fl[min(8 * j + g, count - 1)];
+                    slice_products<XF32, NV, NT, false>(codes, scale, act, plane, lane, bf16, acc);
+                }
+            }
+            slot = S::SLOT - slot;
         }
-        slot = slot == DEPTH - 1 ? 0 : slot + 1;
+        if (p.parts == 1 && tile < tile_hi) {
+            const uint32_t row = tile / 8 * ATOM + 4 * (tile % 8) + (g & 3u) + 64 * (g >> 2);    // this lane's: and + 32
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    store_y<NV>(p, t0 + 8 * i + 2 * t + (j & 1), row + 32 * (j >> 1), acc[i][j]);
+                    acc[i][j] = 0.0f;
+                }
+        }
     }
+    if (p.parts == 1) return;
 
-    // the sums of this CTA, [token][row], over the ring (all its copies have landed)
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
-    const uint32_t r_lo = 4 * warp + (g & 3u) + 64 * (g >> 2);    // this lane's rows: r_lo and r_lo + 32
-    float *sums = reinterpret_cast<float *>(smem);
+    // One pass: the parts' sums, [token][place in the tile] in each warp's ring (its copies have landed)
+    __syncwarp();
+    float *sums = reinterpret_cast<float *>(ring);
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sums[(8 * i + 2 * t + (j & 1)) * ROWS + r_lo + 32 * (j >> 1)] = acc[i][j];
-    if (split > 1) cg::this_cluster().sync();
-    else __syncthreads();
-    for (uint32_t e = rank * THREADS + tid; e < NT * 8 * ROWS; e += split * THREADS) {
-        const uint32_t tok = t0 + e / ROWS, row = row0 + e % ROWS;
-        if (tok >= p.tokens || row >= p.n) continue;
+        for (int j = 0; j < 4; ++j) sums[(8 * i + 2 * t + (j & 1)) * 16 + g + 8 * (j >> 1)] = acc[i][j];
+    __syncthreads();
+    const uint32_t mine = min(tile_hi - tile_lo, p.lanes) * 16;
+    for (uint32_t e = threadIdx.x; e < count * mine; e += blockDim.x) {
+        const uint32_t ti = e / mine, c = e % mine / 16, q = e % 16, at = tile_lo + c;
         float v = 0.0f;
-        for (uint32_t c = 0; c < split; ++c) v += cg::this_cluster().map_shared_rank(sums, c)[e];
-        v *= NV ? __fdiv_rn(p.alpha, p.enc[row / p.lines]) : p.alpha;
-        const int64_t off = static_cast<int64_t>(tok) * p.ldy + row;
-        if (p.y_f32) static_cast<float *>(p.y)[off] = v;
-        else static_cast<__nv_bfloat16 *>(p.y)[off] = __float2bfloat16_rn(v);
+        for (uint32_t k = 0; k < p.parts; ++k)
+            v += reinterpret_cast<const float *>(smem + (k * p.lanes + c) * S::RING)[ti * 16 + q];
+        const uint32_t row = at / 8 * ATOM + 4 * (at % 8) + (q & 3u) + 64 * ((q >> 2) & 1u) + 32 * (q >> 3);
+        store_y<NV>(p, t0 + ti, row, v);
     }
-    if (split > 1) cg::this_cluster().sync();              // the others still read this CTA's sums
 }
 
 template <bool XF32, bool NV, int NT>
-cudaError_t launch(const GemvParams &p, int split, cudaStream_t st) {
+cudaError_t launch(GemvParams &p, int sms, cudaStream_t st) {
+    using S = Shape<XF32, NV, NT>;
     static std::atomic<uint64_t> done{0};
     auto kern = gemv_kernel<XF32, NV, NT>;
-    constexpr int SMEM = Shape<XF32, NV, NT>::SMEM;
-    const cudaError_t e = ensure_smem_limit(kern, SMEM, done);
+    const cudaError_t e = ensure_smem_limit(kern, SMEM_MAX, done);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((p.n + ROWS - 1) / ROWS * split, (p.tokens + 8 * NT - 1) / (8 * NT));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = split;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
-// CTAs that share a row block.
-int choose_split(uint32_t blocks, uint32_t slices) {
-    if (const char *e = std::getenv("GV_SPLIT")) return std::atoi(e);
-    int c = 1;
-    while (c < 8 && blocks * c < 296 && static_cast<uint32_t>(2 * c) <= slices) c *= 2;
-    return c;
+    p.tile = p.tokens < 8 * NT ? p.tokens : 8 * NT;
+    const uint32_t grid = p.tiles < static_cast<uint32_t>(sms) ? p.tiles : sms;
+    const uint32_t most = (p.tiles + grid - 1) / grid;             // tiles of a CTA
+    p.passes = (most + MAX_WARPS - 1) / MAX_WARPS;
+    p.lanes = (most + p.passes - 1) / p.passes;
+    p.parts = 1;
+    if (p.passes == 1) {
+        // as many as there are warps for, and room for a step's activations of the most
+        // tokens a CTA can have (so that the split does not depend on their number)
+        constexpr int MOST_NT = XF32 ? 1 : 2;
+        uint32_t fit = MAX_WARPS / p.lanes;
+        while (fit > 1 && Shape<XF32, NV, MOST_NT>::smem(p.lanes * fit, 8 * MOST_NT, fit) > SMEM_MAX) --fit;
+        p.steps = (p.slices + fit - 1) / fit;
+        p.parts = (p.slices + p.steps - 1) / p.steps;
+    }
+    p.steps = (p.slices + p.parts - 1) / p.parts;
+    const uint32_t warps = p.lanes * p.parts;
+    // as many steps' activations at a time as fit: the largest window that makes their number small
+    uint32_t windows = 1;
+    for (p.window = p.steps; p.window > 1 && S::smem(warps, p.tile, p.window * p.parts) > SMEM_MAX;
+         p.window = (p.steps + windows - 1) / windows)
+        ++windows;
+    kern<<<dim3(grid, (p.tokens + 8 * NT - 1) / (8 * NT)), 32 * warps, S::smem(warps, p.tile, p.window * p.parts), st>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace mxgemv
@@ -470,11 +515,13 @@ cudaError_t mx_launch_gemv(const MxGemvArgs &a, cudaStream_t st) {
     p.k_blocks = p.k / (a.enc ? 16 : 32);
     p.k_groups = (p.k_blocks + 3) / 4;
     p.slices = (p.k + SLICE - 1) / SLICE;
-    p.words = p.k_blocks % 4 == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 3u) == 0;
+    p.words = a.sl != SL_PLAIN || (p.k_blocks % 4 == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 3u) == 0);
+    p.full = p.words && p.k % 32 == 0 ? p.k / SLICE : 0;
+    const uint32_t rest = p.n % ATOM;                              // rows of the last atom: a tile starts at each 4th of the first 32
+    p.tiles = p.n / ATOM * 8 + (rest >= 32 ? 8 : (rest + 3) / 4);
     p.alpha = a.alpha; p.y = a.y; p.y_f32 = a.ydt == MX_F32; p.ldy = a.ldy;
-    const int split = choose_split((p.n + ROWS - 1) / ROWS, p.slices);
     const bool nv = a.enc != nullptr;
-    if (a.xdt == MX_F32) return nv ? launch<true, true, 1>(p, split, st) : launch<true, false, 1>(p, split, st);
-    if (p.tokens <= 8) return nv ? launch<false, true, 1>(p, split, st) : launch<false, false, 1>(p, split, st);
-    return nv ? launch<false, true, 2>(p, split, st) : launch<false, false, 2>(p, split, st);
+    if (a.xdt == MX_F32) return nv ? launch<true, true, 1>(p, a.num_sms, st) : launch<true, false, 1>(p, a.num_sms, st);
+    if (p.tokens <= 8) return nv ? launch<false, true, 1>(p, a.num_sms, st) : launch<false, false, 1>(p, a.num_sms, st);
+    return nv ? launch<false, true, 2>(p, a.num_sms, st) : launch<false, false, 2>(p, a.num_sms, st);
 }

@@ -365,42 +365,77 @@ def gemm_quantize(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.
     return codes, scales
 
 
-def _on(device: int, t: torch.Tensor, what: str) -> torch.Tensor:
-    if not t.is_cuda or t.get_device() != device:
+# The checks of the calls below.  They read each tensor attribute once: a
+# decoding step makes these calls for every layer and token, and on tensors of
+# a few kilobytes the host's part is most of their time.
+
+def _device(t: torch.Tensor, what: str) -> int:
+    """The index of t's device, which has to be the current one."""
+    device = t.get_device()
+    if device < 0 or device != torch.cuda.current_device():
         raise ValueError(f"{what} must be on the current CUDA device")
-    return t
+    return device
+
+
+def _elsewhere(what: str):
+    raise ValueError(f"{what} must be on the same CUDA device as the other tensors")
+
+
+def _first(t: torch.Tensor, what: str):
+    """Check the 2-D tensor that gives a call its device, type and sizes;
+    returns (device, dtype code, shape, leading dimension)."""
+    dt = DTYPE.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{what} must be float32 or bfloat16")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{what} must be 2-D with unit column stride")
+    return _device(t, what), dt, shape, strides[0] if shape[0] > 1 else shape[1]
 
 
 def _matrix(device: int, t: torch.Tensor, what: str, shape, dtype) -> int:
     """Check a 2-D row-pitched tensor; returns its leading dimension."""
-    _on(device, t, what)
-    if t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} must be {shape[0]} x {shape[1]} with unit column stride")
+    if t.get_device() != device:
+        _elsewhere(what)
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}")
-    return t.stride(0) if shape[0] > 1 else shape[1]
+    strides = t.stride()
+    if t.shape != shape or (strides[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{what} must be {shape[0]} x {shape[1]} with unit column stride")
+    return strides[0] if shape[0] > 1 else shape[1]
 
 
-def _flat(device: int, t: torch.Tensor, what: str, n: int, dtype) -> torch.Tensor:
-    """Check a contiguous buffer of at least n values."""
-    _on(device, t, what)
+def _flat(device: int, t: torch.Tensor, what: str, n: int, dtype) -> int:
+    """Check a contiguous buffer of at least n values; returns its address."""
+    if t.get_device() != device:
+        _elsewhere(what)
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}")
     if t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous and hold {n} values")
-    return t
+    return t.data_ptr()
 
 
-def _here(x: torch.Tensor) -> int:
-    """The index of x's device, which has to be the current one."""
-    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
-        raise ValueError("x must be on the current CUDA device")
-    return x.get_device()
+def _weight(device: int, t: torch.Tensor, cols: int):
+    """Check a norm's weight; returns (address, dtype code)."""
+    if t.get_device() != device:
+        _elsewhere("weight")
+    dt = DTYPE.get(t.dtype)
+    if dt is None:
+        raise TypeError("weight must be float32 or bfloat16")
+    if t.numel() != cols or not t.is_contiguous():
+        raise ValueError(f"weight must be contiguous and hold {cols} values")
+    return t.data_ptr(), dt
 
 
 def _allocating(stream):
     """New tensors belong to the stream that the call runs on."""
     return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _handle(stream, device: int) -> int:
+    """The stream's handle; of the current stream without a Stream object."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _ptr(t) -> int | None:
@@ -409,44 +444,32 @@ def _ptr(t) -> int | None:
 
 def _norm_args(x, weight, residual, h, y, want_y, rstd, want_rstd, stream):
     """Checks and allocations that the norm's two forms share."""
-    if x.dim() != 2 or x.stride(1) != 1:
-        raise ValueError("x must be 2-D with unit column stride")
-    if x.dtype not in DTYPE:
-        raise TypeError("x must be float32 or bfloat16")
-    dev = _here(x)
-    rows, cols = shape = x.shape
-    _on(dev, weight, "weight")
-    if weight.dtype not in DTYPE:
-        raise TypeError("weight must be float32 or bfloat16")
-    if weight.numel() != cols or not weight.is_contiguous():
-        raise ValueError(f"weight must be contiguous and hold {cols} values")
-    if residual is None and h is not None:
-        raise ValueError("h is written only with a residual")
-    new = []
-    if residual is not None and h is None:
-        new.append("h")
-    if want_y and y is None:
-        new.append("y")
-    if want_rstd and rstd is None:
-        new.append("rstd")
-    if new:
+    dev, xdt, shape, ldx = _first(x, "x")
+    rows, cols = shape
+    w, wdt = _weight(dev, weight, cols)
+    new_h, new_y, new_rstd = residual is not None and h is None, want_y and y is None, want_rstd and rstd is None
+    if new_h or new_y or new_rstd:
         with _allocating(stream):
-            if "h" in new:
+            if new_h:
                 h = torch.empty(shape, dtype=x.dtype, device=x.device)
-            if "y" in new:
+            if new_y:
                 y = torch.empty(shape, dtype=x.dtype, device=x.device)
-            if "rstd" in new:
+            if new_rstd:
                 rstd = torch.empty((rows,), dtype=torch.float32, device=x.device)
-    ldx = x.stride(0) if rows > 1 else cols
+    r = hp = yp = rp = None
     ldr = ldh = ldy = 0
     if residual is not None:
         ldr = _matrix(dev, residual, "residual", shape, x.dtype)
         ldh = _matrix(dev, h, "h", shape, x.dtype)
+        r, hp = residual.data_ptr(), h.data_ptr()
+    elif h is not None:
+        raise ValueError("h is written only with a residual")
     if y is not None:
         ldy = _matrix(dev, y, "y", shape, x.dtype)
+        yp = y.data_ptr()
     if rstd is not None:
-        _flat(dev, rstd, "rstd", rows, torch.float32)
-    return dev, rows, cols, ldx, ldr, h, ldh, y, ldy, rstd
+        rp = _flat(dev, rstd, "rstd", rows, torch.float32)
+    return (x.data_ptr(), xdt, rows, cols, ldx, r, ldr, w, wdt), (hp, ldh, yp, ldy, rp), dev, h, y, rstd
 
 
 def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,
@@ -459,11 +482,10 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: 
     asked for).  `out` may supply the three; h may be x or the residual itself
     and y may be x."""
     y, h, rstd = out if out is not None else (None, None, None)
-    _, rows, cols, ldx, ldr, h, ldh, y, ldy, rstd = _norm_args(x, weight, residual, h, y, True, rstd, with_rstd,
-                                                               stream)
-    rc = lib().mx_rmsnorm(x.data_ptr(), DTYPE[x.dtype], rows, cols, ldx, _ptr(residual), ldr, weight.data_ptr(),
-                          DTYPE[weight.dtype], eps, _ptr(h), ldh, y.data_ptr(), ldy, _ptr(rstd), _stream(stream))
-    _check(rc, "mx_rmsnorm")
+    ins, outs, dev, h, y, rstd = _norm_args(x, weight, residual, h, y, True, rstd, with_rstd, stream)
+    rc = (_lib or lib()).mx_rmsnorm(*ins, eps, *outs, _handle(stream, dev))
+    if rc != MX_OK:
+        raise MxError(rc, "mx_rmsnorm")
     return y, h, rstd
 
 
@@ -477,10 +499,10 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
     None unless there is a residual, with_y, with_rstd.  `out` may supply the
     five (None for one that is not wanted or is to be allocated)."""
     codes, scales, h, y, rstd = out if out is not None else (None,) * 5
-    dev, rows, cols, ldx, ldr, h, ldh, y, ldy, rstd = _norm_args(x, weight, residual, h, y, with_y, rstd, with_rstd,
-                                                                 stream)
+    ins, outs, dev, h, y, rstd = _norm_args(x, weight, residual, h, y, with_y, rstd, with_rstd, stream)
     f, sl = _fmt(fmt), _layout(scale_layout)
-    L = lib()
+    L = _lib or lib()
+    rows, cols = ins[2], ins[3]
     n_codes, n_scales = L.mx_codes_bytes(f, rows, cols), L.mx_scales_bytes(sl, rows, cols)
     if codes is None or scales is None:
         with _allocating(stream):
@@ -488,13 +510,12 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
                 codes = torch.empty((rows, codes_row_bytes(f, cols)), dtype=torch.uint8, device=x.device)
             if scales is None:
                 scales = torch.empty(max(n_scales, 1), dtype=torch.uint8, device=x.device)
-    _flat(dev, codes, "codes", n_codes, torch.uint8)
-    _flat(dev, scales, "scales", n_scales, torch.uint8)
-    rc = L.mx_rmsnorm_quantize(x.data_ptr(), DTYPE[x.dtype], rows, cols, ldx, _ptr(residual), ldr,
-                               weight.data_ptr(), DTYPE[weight.dtype], eps, f,
-                               ROUND[rnd] if isinstance(rnd, str) else int(rnd), seed & (2**64 - 1), _ptr(h), ldh,
-                               _ptr(y), ldy, _ptr(rstd), codes.data_ptr(), scales.data_ptr(), sl, _stream(stream))
-    _check(rc, "mx_rmsnorm_quantize")
+    c = _flat(dev, codes, "codes", n_codes, torch.uint8)
+    s = _flat(dev, scales, "scales", n_scales, torch.uint8)
+    rc = L.mx_rmsnorm_quantize(*ins, eps, f, ROUND[rnd] if isinstance(rnd, str) else int(rnd), seed & (2**64 - 1),
+                               *outs, c, s, sl, _handle(stream, dev))
+    if rc != MX_OK:
+        raise MxError(rc, "mx_rmsnorm_quantize")
     return codes, scales, h, y, rstd
 
 
@@ -509,39 +530,30 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rs
     residual, and dweight as fp32.  `out` may supply both (dx may be dy or
     dres), `workspace` the uint8 scratch of rmsnorm_backward_workspace, which
     one call at a time may use."""
-    if dy.dim() != 2 or dy.stride(1) != 1:
-        raise ValueError("dy must be 2-D with unit column stride")
-    if dy.dtype not in DTYPE:
-        raise TypeError("dy must be float32 or bfloat16")
-    dev = _here(dy)
-    rows, cols = shape = dy.shape
+    dev, dt, shape, lddy = _first(dy, "dy")
+    rows, cols = shape
     dx, dweight = out if out is not None else (None, None)
-    L = lib()
+    L = _lib or lib()
     n_ws = L.mx_rmsnorm_backward_workspace_bytes(rows, cols)
-    with _allocating(stream):
-        if dx is None:
-            dx = torch.empty(shape, dtype=dy.dtype, device=dy.device)
-        if dweight is None:
-            dweight = torch.empty((cols,), dtype=torch.float32, device=dy.device)
-        if workspace is None:
-            workspace = torch.empty(max(n_ws, 1), dtype=torch.uint8, device=dy.device)
-    lddy = dy.stride(0) if rows > 1 else cols
+    if dx is None or dweight is None or workspace is None:
+        with _allocating(stream):
+            if dx is None:
+                dx = torch.empty(shape, dtype=dy.dtype, device=dy.device)
+            if dweight is None:
+                dweight = torch.empty((cols,), dtype=torch.float32, device=dy.device)
+            if workspace is None:
+                workspace = torch.empty(max(n_ws, 1), dtype=torch.uint8, device=dy.device)
     ldh = _matrix(dev, h, "h", shape, dy.dtype)
     lddx = _matrix(dev, dx, "dx", shape, dy.dtype)
     lddres = _matrix(dev, dres, "dres", shape, dy.dtype) if dres is not None else 0
-    _on(dev, weight, "weight")
-    if weight.dtype not in DTYPE:
-        raise TypeError("weight must be float32 or bfloat16")
-    if weight.numel() != cols or not weight.is_contiguous():
-        raise ValueError(f"weight must be contiguous and hold {cols} values")
-    _flat(dev, rstd, "rstd", rows, torch.float32)
-    _flat(dev, dweight, "dweight", cols, torch.float32)
-    _flat(dev, workspace, "workspace", n_ws, torch.uint8)
-    rc = L.mx_rmsnorm_backward(dy.data_ptr(), DTYPE[dy.dtype], rows, cols, lddy, h.data_ptr(), ldh,
-                               weight.data_ptr(), DTYPE[weight.dtype], rstd.data_ptr(), _ptr(dres), lddres,
-                               dx.data_ptr(), lddx, dweight.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                               _stream(stream))
-    _check(rc, "mx_rmsnorm_backward")
+    w, wdt = _weight(dev, weight, cols)
+    rp = _flat(dev, rstd, "rstd", rows, torch.float32)
+    dwp = _flat(dev, dweight, "dweight", cols, torch.float32)
+    wsp = _flat(dev, workspace, "workspace", n_ws, torch.uint8)
+    rc = L.mx_rmsnorm_backward(dy.data_ptr(), dt, rows, cols, lddy, h.data_ptr(), ldh, w, wdt, rp, _ptr(dres),
+                               lddres, dx.data_ptr(), lddx, dwp, wsp, workspace.numel(), _handle(stream, dev))
+    if rc != MX_OK:
+        raise MxError(rc, "mx_rmsnorm_backward")
     return dx, dweight
 
 
@@ -553,19 +565,18 @@ def rmsnorm_backward_workspace(rows: int, cols: int, device=None) -> torch.Tenso
 
 def _gemv_args(x, N, K, out_dtype, out, stream):
     """Checks and allocations that the two weight formats share."""
-    if x.dim() != 2 or x.shape[1] != K or (K > 1 and x.stride(1) != 1):
-        raise ValueError("x must be 2-D, K columns with unit stride")
-    if x.dtype not in DTYPE:
-        raise TypeError("x must be float32 or bfloat16")
-    dev = _here(x)
-    M = x.shape[0]
+    dev, xdt, shape, ldx = _first(x, "x")
+    if shape[1] != K:
+        raise ValueError("x must have K columns")
+    M = shape[0]
     if out is None:
         with _allocating(stream):
             out = torch.empty((M, N), dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
-    if out.dtype not in DTYPE:
+    ydt = DTYPE.get(out.dtype)
+    if ydt is None:
         raise TypeError("the output must be float32 or bfloat16")
     ldy = _matrix(dev, out, "out", (M, N), out.dtype)
-    return dev, M, x.stride(0) if M > 1 else K, out, ldy
+    return dev, out, (x.data_ptr(), xdt, ldx, M, N, K), (out.data_ptr(), ydt, ldy)
 
 
 def gemv(w_codes: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, N: int, K: int, fmt="e2m1",
@@ -576,13 +587,13 @@ def gemv(w_codes: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, N: int,
     in `scale_layout`, the buffers gemm takes as its B operand.  The output has
     x's type unless out_dtype or `out` says otherwise."""
     f, sl = _fmt(fmt), _layout(scale_layout)
-    dev, M, ldx, out, ldy = _gemv_args(x, N, K, out_dtype, out, stream)
-    L = lib()
-    _flat(dev, w_codes, "w_codes", L.mx_codes_bytes(f, N, K), torch.uint8)
-    _flat(dev, w_scales, "w_scales", L.mx_scales_bytes(sl, N, K), torch.uint8)
-    rc = L.mx_gemv(w_codes.data_ptr(), w_scales.data_ptr(), f, sl, x.data_ptr(), DTYPE[x.dtype], ldx, M, N, K,
-                   alpha, out.data_ptr(), DTYPE[out.dtype], ldy, _stream(stream))
-    _check(rc, "mx_gemv")
+    dev, out, ins, outs = _gemv_args(x, N, K, out_dtype, out, stream)
+    L = _lib or lib()
+    c = _flat(dev, w_codes, "w_codes", L.mx_codes_bytes(f, N, K), torch.uint8)
+    s = _flat(dev, w_scales, "w_scales", L.mx_scales_bytes(sl, N, K), torch.uint8)
+    rc = L.mx_gemv(c, s, f, sl, *ins, alpha, *outs, _handle(stream, dev))
+    if rc != MX_OK:
+        raise MxError(rc, "mx_gemv")
     return out
 
 
@@ -593,15 +604,14 @@ def gemv_nvfp4(w, x: torch.Tensor, N: int, K: int, domain_rows: int = 0, alpha: 
     `scale_layout`."""
     codes, scales, enc = w
     sl = _layout(scale_layout)
-    dev, M, ldx, out, ldy = _gemv_args(x, N, K, out_dtype, out, stream)
-    L = lib()
-    _flat(dev, codes, "codes", N * K // 2, torch.uint8)
-    _flat(dev, scales, "scales", L.mx_nvfp4_scales_bytes(sl, N, K), torch.uint8)
-    _flat(dev, enc, "enc_scales", L.mx_nvfp4_domains(N, domain_rows), torch.float32)
-    rc = L.mx_gemv_nvfp4(codes.data_ptr(), scales.data_ptr(), enc.data_ptr(), domain_rows, sl, x.data_ptr(),
-                         DTYPE[x.dtype], ldx, M, N, K, alpha, out.data_ptr(), DTYPE[out.dtype], ldy,
-                         _stream(stream))
-    _check(rc, "mx_gemv_nvfp4")
+    dev, out, ins, outs = _gemv_args(x, N, K, out_dtype, out, stream)
+    L = _lib or lib()
+    c = _flat(dev, codes, "codes", N * K // 2, torch.uint8)
+    s = _flat(dev, scales, "scales", L.mx_nvfp4_scales_bytes(sl, N, K), torch.uint8)
+    e = _flat(dev, enc, "enc_scales", L.mx_nvfp4_domains(N, domain_rows), torch.float32)
+    rc = L.mx_gemv_nvfp4(c, s, e, domain_rows, sl, *ins, alpha, *outs, _handle(stream, dev))
+    if rc != MX_OK:
+        raise MxError(rc, "mx_gemv_nvfp4")
     return out
 
 
