@@ -3,10 +3,12 @@
 // E4M3 scale per 16 and an fp32 encode scale per domain of rows), x in bf16 or
 // fp32 as it is.  The weights' buffers are the block-scaled GEMM's operands.
 //
-// The weight rows are cut into tiles of 16 and the tiles dealt out evenly, one
-// CTA per SM; inside a CTA a warp takes a tile, or a part of K of a tile where
-// there are fewer tiles than warps (the parts' sums are added in order through
-// shared memory).  A warp walks along its K in slices of 256 codes, 128 bytes
+// The weight rows are cut into tiles of 16 and the tiles dealt out evenly over
+// the clusters of CTAs, one CTA per SM; a warp takes a tile, or a part of K of
+// a tile where there are fewer tiles than warps.  The parts of a tile are spread
+// over its cluster's CTAs, so that each stages the activations of its parts
+// alone, and their sums are added in order through (distributed) shared memory.
+// A warp walks along its K in slices of 256 codes, 128 bytes
 // of each row, copied asynchronously into its own ring, so that warps wait for
 // one another only where activations are staged.  It multiplies its 16 rows
 // with eight tokens at a time by m16n8k16 tensor-core products with fp32 sums,
@@ -22,8 +24,10 @@
 //  - fp32 activations are split into three bf16 terms (8 + 8 + 8 bits, by
 //    truncation, exact down to bf16's smallest subnormal) whose products go
 //    into the same sum.
-// The split of the work depends on N and K alone, and a token is a column of
-// its own, so a token's result does not depend on the other tokens.
+// The number of parts depends on N and K alone, and a token is a column of its
+// own, so a token's result does not depend on the other tokens.
+#include <algorithm>
+#include <cooperative_groups.h>
 #include <cstdint>
 #include <type_traits>
 #include <cuda_bf16.h>
@@ -36,12 +40,13 @@
 namespace mxgemv {
 
 using namespace mxk;
+namespace cg = cooperative_groups;
 
 constexpr int ATOM = 128;            // weight rows of a scale atom: eight tiles
 constexpr int SLICE = 256;           // codes of a row per slice
 constexpr int DEPTH = 2;             // slices in a warp's ring
 constexpr int PITCH = SLICE / 2 + 16;      // bytes of a row's slice in the ring: eight rows' words in different banks
-constexpr int MAX_WARPS = 32;
+constexpr int MAX_WARPS = 28;
 constexpr int SMEM_MAX = 227 * 1024;
 
 struct GemvParams {
@@ -57,7 +62,11 @@ struct GemvParams {
     uint32_t tile;             // tokens of a CTA: min(tokens, 8 NT)
     uint32_t k_blocks, k_groups, slices;
     uint32_t tiles;            // of 16 rows
-    uint32_t lanes, parts;     // a CTA's warps: tiles at a time x parts of K
+    uint32_t lanes, parts;     // tiles of a cluster at a time, parts of K of a tile
+    uint32_t share;            // a CTA's parts: it has lanes x share warps
+    uint32_t lanes_inv, share_inv;      // 2^32 over them, rounded up: quotients of small numbers
+    uint32_t size_log;         // CTAs of a cluster: 2^size_log
+    uint32_t each, extra;      // tiles of a cluster, one more of the first `extra`
     uint32_t passes;           // times `lanes` tiles
     uint32_t steps;            // slices of a warp: ceil(slices / parts)
     uint32_t window;           // steps whose activations are staged together
@@ -212,7 +221,7 @@ __device__ __forceinline__ void slice_products(const uint8_t *codes, uint32_t sc
     float f_lo[2] = {1.0f, 1.0f}, f_hi[2] = {1.0f, 1.0f};
     uint32_t m_lo[2], m_hi[2];
     if (NV && EXACT16) f_lo[0] = f_lo[1] = f_hi[0] = f_hi[1] = ACT_DOWN;
-#pragma unroll(EXACT16 ? 8 : 2)
+#pragma unroll
     for (int c = 0; c < 8; ++c) {
         if (c % (NV ? 2 : 4) == 0)
             asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(words.x), "=r"(words.y) : "r"(scale + c / (NV ? 2 : 4) * 64));
@@ -264,6 +273,9 @@ __device__ __forceinline__ void slice_products(const uint8_t *codes, uint32_t sc
     }
 }
 
+// a / b for a, b < 2^16, inv = ceil(2^32 / b) (0 for b = 1): inv * b - 2^32 < b, so the product is off by less than a
+__device__ __forceinline__ uint32_t small_quotient(uint32_t a, uint32_t inv) { return inv ? __umulhi(a, inv) : a; }
+
 template <bool NV>
 __device__ __forceinline__ void store_y(const GemvParams &p, uint32_t tok, uint32_t row, float v) {
     if (tok >= p.tokens || row >= p.n) return;
@@ -274,12 +286,12 @@ __device__ __forceinline__ void store_y(const GemvParams &p, uint32_t tok, uint3
 }
 
 template <bool XF32, bool NV, int NT>
-__global__ void __launch_bounds__(32 * MAX_WARPS) gemv_kernel(const __grid_constant__ GemvParams p) {
+__global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_constant__ GemvParams p) {
     using S = Shape<XF32, NV, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const uint32_t g = lane >> 2, t = lane & 3u;
-    const uint32_t win = p.window * p.parts;                   // slices in a window
+    const uint32_t win = p.window * p.share;                   // slices in a window
     const uint32_t pitch = S::token(win), plane = p.tile * pitch;
     uint8_t *ring = smem + warp * S::RING;                     // this warp's
     uint8_t *acts = smem + warps * S::RING;                    // [planes][tile][pitch]
@@ -287,94 +299,125 @@ __global__ void __launch_bounds__(32 * MAX_WARPS) gemv_kernel(const __grid_const
     const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
 
     const uint32_t t0 = blockIdx.y * (8 * NT), count = min(p.tokens - t0, 8u * NT);
-    const uint32_t tile_lo = static_cast<uint32_t>(static_cast<uint64_t>(p.tiles) * blockIdx.x / gridDim.x);
-    const uint32_t tile_hi = static_cast<uint32_t>(static_cast<uint64_t>(p.tiles) * (blockIdx.x + 1) / gridDim.x);
-    const uint32_t col = warp % p.lanes, part = warp / p.lanes;
+    const uint32_t size = 1u << p.size_log, rank = blockIdx.x & (size - 1), cluster = blockIdx.x >> p.size_log;
+    const uint32_t tile_lo = cluster * p.each + min(cluster, p.extra);
+    const uint32_t tile_hi = tile_lo + p.each + (cluster < p.extra ? 1u : 0u);
+    const uint32_t here = small_quotient(warp, p.lanes_inv), col = warp - here * p.lanes, part = rank * p.share + here;
     const uint32_t row_bytes = p.k / 2;
 
     // A tile is the rows 4 w + {0..3} + {0, 32, 64, 96} of a scale atom, a 64-byte
-    // run of each of its 512-byte groups.  Lane (r, chunk) copies 16 bytes of
-    // four rows to the places r + {0, 8, 4, 12} of the slot, so that lane (g, t)
-    // finds its two rows at places g and g + 8.  A row past the last reads the
-    // last one again; its results are not stored.
-    const uint32_t chunk = lane & 7u, r0 = lane >> 3;
-    const uint32_t cdst = ring32 + r0 * PITCH + chunk * 16;
+    // run of each of its 512-byte groups.  Place g of a slot holds row
+    // g % 4 + 64 (g / 4), place g + 8 the row 32 behind it: the rows of lane
+    // (g, t) in the products, and those whose 16-byte pieces t and t + 4 it
+    // copies.  A row past the last reads the last one again; its results are
+    // not stored.
+    const uint32_t cdst = ring32 + g * PITCH + t * 16;
     // lane l copies scale word l % 16 (of rows r + 32 q: 4 r + q) of group l / 16
     const uint32_t word = lane & 15u, sgroup = lane >> 4;
     const uint32_t sstep = p.sl == SL_PLAIN ? 4u : (p.sl == SL_MMA ? 512u : 2048u);     // bytes between groups
     const uint32_t sdst = ring32 + 16 * PITCH + lane * 4;
-    const uint8_t *codes0;
-    uint32_t src[4], ssrc;          // 32-bit offsets: 128 rows are at most 2^30 bytes, scale buffers below 4 GiB
+    const uint8_t *src_lo, *src_hi, *src_s;                    // this lane's pieces of the next slice
     auto set_tile = [&](uint32_t tile) {
-        const uint32_t row0 = tile / 8 * ATOM, w = tile % 8;
-        codes0 = p.codes + static_cast<int64_t>(row0) * row_bytes;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) src[i] = (min(row0 + 4 * w + r0 + 32 * i, p.n - 1) - row0) * row_bytes + chunk * 16;
+        const uint32_t row0 = tile / 8 * ATOM, w = tile % 8, row = row0 + 4 * w + (g & 3u) + 64 * (g >> 2);
+        const int64_t at = static_cast<int64_t>(part) * (SLICE / 2) + t * 16;
+        src_lo = p.codes + static_cast<int64_t>(min(row, p.n - 1)) * row_bytes + at;
+        src_hi = p.codes + static_cast<int64_t>(min(row + 32, p.n - 1)) * row_bytes + at;
         const uint32_t srow = min(row0 + 4 * w + (word >> 2) + 32 * (word & 3u), p.n - 1);
-        ssrc = (p.sl == SL_PLAIN ? srow * p.k_blocks : tile / 8 * p.k_groups * sstep + 64 * w + 4 * word) + sgroup * sstep;
+        src_s = p.scales + (part * S::GROUPS + sgroup) * static_cast<uint64_t>(sstep) +
+                (p.sl == SL_PLAIN ? static_cast<uint64_t>(srow) * p.k_blocks
+                                  : static_cast<uint64_t>(tile / 8) * p.k_groups * sstep + 64 * w + 4 * word);
     };
+    const uint32_t code_step = p.parts * (SLICE / 2), scale_step = p.parts * S::GROUPS * sstep;
     auto issue = [&](uint32_t s, uint32_t slot) {
-        const uint32_t at = s * (SLICE / 2);
         if (s < p.full) {                                      // (uniform) a whole slice of 16-byte pieces and words
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                copy_async<16>(cdst + slot + (8 * (i & 1) + 4 * (i >> 1)) * PITCH, codes0 + (src[i] + at));
+            for (int i = 0; i < 2; ++i) {
+                copy_async<16>(cdst + slot + i * 64, src_lo + i * 64);
+                copy_async<16>(cdst + slot + 8 * PITCH + i * 64, src_hi + i * 64);
+            }
 #pragma unroll
-            for (int i = 0; i < S::GROUPS / 2; ++i)
-                copy_async<4>(sdst + slot + i * 128, p.scales + (ssrc + (s * S::GROUPS + 2 * i) * sstep));
-            return;
-        }
-        // the end of K, rows of an odd number of 8-byte blocks, or scale rows off the words
-        const uint32_t b = at + chunk * 16, left = b < row_bytes ? row_bytes - b : 0u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t dst = cdst + slot + (8 * (i & 1) + 4 * (i >> 1)) * PITCH;
-            const uint8_t *from = codes0 + (src[i] + at);
-            copy_async_part<8>(dst, left ? from : p.codes, left ? 8u : 0u);
-            copy_async_part<8>(dst + 8, left > 8 ? from + 8 : p.codes, left > 8 ? 8u : 0u);
-        }
+            for (int i = 0; i < S::GROUPS / 2; ++i) copy_async<4>(sdst + slot + i * 128, src_s + 2 * i * sstep);
+        } else {
+            // the end of K, rows of an odd number of 8-byte blocks, or scale rows off the words
 #pragma unroll 1
-        for (int i = 0; i < S::GROUPS / 2; ++i) {
-            const uint32_t kg = s * S::GROUPS + sgroup + 2 * i;
-            const uint32_t n = kg * 4 < p.k_blocks ? min(p.k_blocks - kg * 4, 4u) : 0u;   // scales of this word
-            const uint8_t *from = p.scales + (n ? ssrc + (s * S::GROUPS + 2 * i) * sstep : 0u);
-            if (p.words) {
-                copy_async_part<4>(sdst + slot + i * 128, from, n);
-            } else {
-                uint32_t w = 0;
-                for (uint32_t j = 0; j < n; ++j) w |= static_cast<uint32_t>(__ldg(from + j)) << (8 * j);
-                *reinterpret_cast<uint32_t *>(ring + slot + 16 * PITCH + lane * 4 + i * 128) = w;
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t b = s * (SLICE / 2) + t * 16 + (i >> 1) * 64, left = b < row_bytes ? row_bytes - b : 0u;
+                const uint32_t dst = cdst + slot + (i & 1) * (8 * PITCH) + (i >> 1) * 64;
+                const uint8_t *from = (i & 1 ? src_hi : src_lo) + (i >> 1) * 64;
+                copy_async_part<8>(dst, left ? from : p.codes, left ? 8u : 0u);
+                copy_async_part<8>(dst + 8, left > 8 ? from + 8 : p.codes, left > 8 ? 8u : 0u);
+            }
+#pragma unroll 1
+            for (int i = 0; i < S::GROUPS / 2; ++i) {
+                const uint32_t kg = s * S::GROUPS + sgroup + 2 * i;
+                const uint32_t n = kg * 4 < p.k_blocks ? min(p.k_blocks - kg * 4, 4u) : 0u;   // scales of this word
+                const uint8_t *from = n ? src_s + 2 * i * sstep : p.scales;
+                if (p.words) {
+                    copy_async_part<4>(sdst + slot + i * 128, from, n);
+                } else {
+                    uint32_t w = 0;
+                    for (uint32_t j = 0; j < n; ++j) w |= static_cast<uint32_t>(__ldg(from + j)) << (8 * j);
+                    *reinterpret_cast<uint32_t *>(ring + slot + 16 * PITCH + lane * 4 + i * 128) = w;
+                }
             }
         }
+        src_lo += code_step;
+        src_hi += code_step;
+        src_s += scale_step;
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
-    // Activations of the window's slices from s0: a warp takes a (token, slice)
-    // at a time, lane l the eight values from 8 l.
-    auto stage = [&](uint32_t s0) {
-        const uint32_t n = min(win, p.slices - s0);
-        uint32_t tok = warp / n, j = warp % n;
+    // Activations of the window's steps from w0, the slices of this CTA's parts:
+    // a warp takes a (token, slice) at a time, lane l the eight values from 8 l.
+    // Returns whether one of this warp's stayed bf16.
+    auto stage = [&](uint32_t w0) {
+        bool any = false;
+        constexpr int BATCH = XF32 ? 2 : 4;                    // loads in flight
+        const uint32_t n = min(p.window, p.steps - w0) * p.share;
+        uint32_t tok = 0, j = warp;
+        auto settle = [&] {
+            while (j >= n && tok < count) {
+                j -= n;
+                ++tok;
+            }
+        };
+        settle();
         while (tok < count) {
-            const uint32_t k = (s0 + j) * SLICE + lane * 8;
-            const int64_t off = static_cast<int64_t>(t0 + tok) * p.ldx + k;
-            uint8_t *dst = acts + tok * pitch + j * (SLICE * 2) + lane * 16;
-            uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-            if (k < p.k) {
+            uint4 v[BATCH][XF32 ? 2 : 1];
+            uint32_t to[BATCH], flag[BATCH];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                to[b] = ~0u;
+                if (tok >= count) continue;
+                const uint32_t step = small_quotient(j, p.share_inv);
+                const uint32_t s = (w0 + step) * p.parts + rank * p.share + j - step * p.share, k = s * SLICE + lane * 8;
+                const bool in = s < p.slices && k < p.k;
+                const int64_t off = static_cast<int64_t>(t0 + tok) * p.ldx + k;
+#pragma unroll
+                for (int h = 0; h < (XF32 ? 2 : 1); ++h) {
+                    v[b][h] = make_uint4(0, 0, 0, 0);
+                    if (in)
+                        v[b][h] = XF32 ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(p.x) + off) + h)
+                                       : __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + off));
+                }
+                to[b] = tok * pitch + j * (SLICE * 2) + lane * 16;
+                flag[b] = j * (8 * NT) + tok;
+                j += warps;
+                settle();
+            }
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                if (to[b] == ~0u) break;
                 if (XF32) {
-                    v0 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(p.x) + off));
-                    v1 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(p.x) + off) + 1);
+                    stage_f32(acts + to[b], v[b][0], v[b][XF32], plane);
                 } else {
-                    v0 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + off));
+                    const bool bad = stage_bf16(acts + to[b], v[b][0]);
+                    if (lane == 0) flags[flag[b]] = bad;
+                    any |= bad;
                 }
             }
-            if (XF32) {
-                stage_f32(dst, v0, v1, plane);
-            } else {
-                const bool bad = stage_bf16(dst, v0);
-                if (lane == 0) flags[j * (8 * NT) + tok] = bad;
-            }
-            for (j += warps; j >= n; j -= n) ++tok;
         }
+        return any;
     };
     if (!XF32)
         for (uint32_t i = threadIdx.x; i < win * 8 * NT; i += blockDim.x)      // the tokens that are not there
@@ -389,56 +432,60 @@ __global__ void __launch_bounds__(32 * MAX_WARPS) gemv_kernel(const __grid_const
 #pragma unroll
     for (int i = 0; i < NT; ++i) act_mine[i] = acts + min(8 * i + g, count - 1) * pitch + t * 16;
 
-    // Step i of a pass is slice i * parts + part of tile pass * lanes + col.
+    // Step i of a pass is slice i * parts + part of tile pass * lanes + col; a
+    // warp without a tile, or past the last slice, only waits with the others.
     uint32_t tile = tile_lo + col, slot = 0;
-    if (tile < tile_hi) {
+    const uint32_t mine = tile < tile_hi ? (p.slices - part + p.parts - 1) / p.parts : 0u;    // parts <= slices
+    if (mine) {
         set_tile(tile);
-        if (part < p.slices) issue(part, 0);
+        issue(part, 0);
     }
     commit();
-    for (uint32_t pass = 0; pass < p.passes; ++pass, tile += p.lanes) {
-        uint32_t s = part, s0 = 0, in_window = 0;
-        for (uint32_t i = 0; i < p.steps; ++i, s += p.parts) {
-            if (in_window == 0 && (p.window < p.steps || pass == 0)) {
-                if (i + pass > 0) __syncthreads();             // the last window has been read
-                s0 = i * p.parts;
-                stage(s0);
-                __syncthreads();
+    bool mixed = false;                     // a token of the window is in bf16 somewhere
+    for (uint32_t pass = 0; pass < p.passes; ++pass) {
+        const uint32_t stop = tile < tile_hi ? mine : 0u;
+        const bool more = tile + p.lanes < tile_hi;
+        for (uint32_t w0 = 0; w0 < p.steps; w0 += p.window) {
+            if (p.window < p.steps || pass == 0) {
+                if (w0 + pass > 0) __syncthreads();            // the last window has been read
+                mixed = __syncthreads_or(stage(w0));
             }
-            if (++in_window == p.window) in_window = 0;
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            __syncwarp();                   // slice s is in, the other slot free
-            if (i + 1 < p.steps) {
-                if (tile < tile_hi && s + p.parts < p.slices) issue(s + p.parts, S::SLOT - slot);
-            } else if (tile + p.lanes < tile_hi) {
-                set_tile(tile + p.lanes);
-                if (part < p.slices) issue(part, S::SLOT - slot);
-            }
-            commit();
-            if (tile < tile_hi && s < p.slices) {
+            uint32_t s = w0 * p.parts + part, act_at = here * (SLICE * 2);
+            const uint8_t *fl = flags + here * (8 * NT);
+            const uint32_t w1 = min(w0 + p.window, stop);
+            for (uint32_t i = w0; i < w1; ++i) {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                __syncwarp();               // slice s is in, the other slot free
+                s += p.parts;
+                if (i + 1 < stop) {
+                    issue(s, S::SLOT - slot);
+                } else if (more) {
+                    set_tile(tile + p.lanes);
+                    issue(part, S::SLOT - slot);
+                }
+                commit();
                 const uint8_t *codes = ring + slot + g * PITCH + 4 * t;
                 const uint32_t scale = ring32 + slot + 16 * PITCH + (g & 3u) * 16 + (g >> 2) * 8;
                 const uint8_t *act[NT];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) act[j] = act_mine[j] + (s - s0) * (SLICE * 2);
-                const uint8_t *fl = flags + (s - s0) * (8 * NT);
-                bool bf16[NT];
-                uint64_t any = XF32;
-                if (!XF32) {
+                for (int j = 0; j < NT; ++j) act[j] = act_mine[j] + act_at;
+                bool bf16[NT], slow = XF32;
+                if (mixed) {
+                    uint64_t any = 0;
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) any |= reinterpret_cast<const uint64_t *>(fl)[j];
+                    for (int j = 0; j < NT; ++j) {
+                        any |= reinterpret_cast<const uint64_t *>(fl + (i - w0) * p.share * (8 * NT))[j];
+                        bf16[j] = fl[(i - w0) * p.share * (8 * NT) + min(8 * j + g, count - 1)];
+                    }
+                    slow = __any_sync(0xffffffffu, any != 0);
                 }
-                if (!XF32 && !__any_sync(0xffffffffu, any != 0)) {
-                    slice_products<XF32, NV, NT, !XF32>(codes, scale, act, plane, lane, bf16, acc);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) bf16[j] = XF32 || fl[min(8 * j + g, count - 1)];
-                    slice_products<XF32, NV, NT, false>(codes, scale, act, plane, lane, bf16, acc);
-                }
+                if (XF32 || slow) slice_products<XF32, NV, NT, false>(codes, scale, act, plane, lane, bf16, acc);
+                else slice_products<XF32, NV, NT, !XF32>(codes, scale, act, plane, lane, bf16, acc);
+                slot = S::SLOT - slot;
+                act_at += p.share * (SLICE * 2);
             }
-            slot = S::SLOT - slot;
         }
-        if (p.parts == 1 && tile < tile_hi) {
+        if (p.parts == 1 && stop) {
             const uint32_t row = tile / 8 * ATOM + 4 * (tile % 8) + (g & 3u) + 64 * (g >> 2);    // this lane's: and + 32
 #pragma unroll
             for (int i = 0; i < NT; ++i)
@@ -448,6 +495,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS) gemv_kernel(const __grid_const
                     acc[i][j] = 0.0f;
                 }
         }
+        tile += p.lanes;
     }
     if (p.parts == 1) return;
 
@@ -458,16 +506,47 @@ __global__ void __launch_bounds__(32 * MAX_WARPS) gemv_kernel(const __grid_const
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) sums[(8 * i + 2 * t + (j & 1)) * 16 + g + 8 * (j >> 1)] = acc[i][j];
-    __syncthreads();
-    const uint32_t mine = min(tile_hi - tile_lo, p.lanes) * 16;
-    for (uint32_t e = threadIdx.x; e < count * mine; e += blockDim.x) {
-        const uint32_t ti = e / mine, c = e % mine / 16, q = e % 16, at = tile_lo + c;
+    if (size > 1) cg::this_cluster().sync();
+    else __syncthreads();
+    const uint32_t rows = min(tile_hi - tile_lo, p.lanes) * 16;
+    for (uint32_t e = rank * blockDim.x + threadIdx.x; e < count * rows; e += size * blockDim.x) {
+        const uint32_t ti = e / rows, c = (e - ti * rows) / 16, q = e % 16, at = tile_lo + c;
+        const float *theirs = reinterpret_cast<const float *>(smem + c * S::RING) + ti * 16 + q;
         float v = 0.0f;
-        for (uint32_t k = 0; k < p.parts; ++k)
-            v += reinterpret_cast<const float *>(smem + (k * p.lanes + c) * S::RING)[ti * 16 + q];
+        for (uint32_t r = 0; r < size; ++r) {
+            const float *from = size > 1 ? cg::this_cluster().map_shared_rank(theirs, r) : theirs;
+            for (uint32_t k = 0; k < p.share; ++k) v += from[k * p.lanes * (S::RING / 4)];
+        }
         const uint32_t row = at / 8 * ATOM + 4 * (at % 8) + (q & 3u) + 64 * ((q >> 2) & 1u) + 32 * (q >> 3);
         store_y<NV>(p, t0 + ti, row, v);
     }
+    if (size > 1) cg::this_cluster().sync();                   // the others still read this CTA's sums
+}
+
+uint32_t ceil_div(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
+
+// Clusters of `size` CTAs with all the shared memory that the device runs at a
+// time; asked once for each device.
+template <typename Kern>
+uint32_t max_clusters(Kern kern, int size, int sms) {
+    static std::atomic<uint32_t> known[64][4];
+    int dev = 0, n = 0, log = size == 2 ? 1 : size == 4 ? 2 : 3;
+    if (size == 1) return sms;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (const uint32_t k = known[dev][log].load(std::memory_order_relaxed)) return k;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(32 * MAX_WARPS);
+    cfg.dynamicSmemBytes = SMEM_MAX;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) return 0;
+    known[dev][log].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 template <bool XF32, bool NV, int NT>
@@ -475,32 +554,77 @@ cudaError_t launch(GemvParams &p, int sms, cudaStream_t st) {
     using S = Shape<XF32, NV, NT>;
     static std::atomic<uint64_t> done{0};
     auto kern = gemv_kernel<XF32, NV, NT>;
-    const cudaError_t e = ensure_smem_limit(kern, SMEM_MAX, done);
+    cudaError_t e = ensure_smem_limit(kern, SMEM_MAX, done);
     if (e != cudaSuccess) return e;
     p.tile = p.tokens < 8 * NT ? p.tokens : 8 * NT;
-    const uint32_t grid = p.tiles < static_cast<uint32_t>(sms) ? p.tiles : sms;
-    const uint32_t most = (p.tiles + grid - 1) / grid;             // tiles of a CTA
-    p.passes = (most + MAX_WARPS - 1) / MAX_WARPS;
-    p.lanes = (most + p.passes - 1) / p.passes;
+
+    // Parts of K, from N, K and the device alone: as many as there are warps for
+    // with the tiles spread over all SMs, a multiple of four (or eight) so that
+    // they can be shared out over a cluster.
+    const uint32_t most = ceil_div(p.tiles, sms);                  // tiles per SM
+    uint32_t idle = 1;                                             // SMs for each tile: a cluster's, if there are so many
+    while (idle < 8 && p.tiles <= max_clusters(kern, 2 * idle, sms)) idle *= 2;
     p.parts = 1;
-    if (p.passes == 1) {
-        // as many as there are warps for, and room for a step's activations of the most
-        // tokens a CTA can have (so that the split does not depend on their number)
+    if (most <= MAX_WARPS / 2) {
+        // with room for a step's activations of the most tokens that a CTA can have
         constexpr int MOST_NT = XF32 ? 1 : 2;
-        uint32_t fit = MAX_WARPS / p.lanes;
-        while (fit > 1 && Shape<XF32, NV, MOST_NT>::smem(p.lanes * fit, 8 * MOST_NT, fit) > SMEM_MAX) --fit;
-        p.steps = (p.slices + fit - 1) / fit;
-        p.parts = (p.slices + p.steps - 1) / p.steps;
+        uint32_t fit = MAX_WARPS / most;
+        while (fit > 1 && Shape<XF32, NV, MOST_NT>::smem(most * fit, 8 * MOST_NT, fit) > SMEM_MAX) --fit;
+        p.parts = fit * idle;
+        p.parts = ceil_div(p.slices, ceil_div(p.slices, p.parts));
+        const uint32_t unit = p.parts >= 8 && idle == 8 ? 8 : p.parts >= 4 ? 4 : 1;
+        p.parts = p.parts / unit * unit;
     }
-    p.steps = (p.slices + p.parts - 1) / p.parts;
-    const uint32_t warps = p.lanes * p.parts;
-    // as many steps' activations at a time as fit: the largest window that makes their number small
+    p.steps = ceil_div(p.slices, p.parts);
+
+    // CTAs of a cluster: as many as make the parts fit and leave no SM idle, and
+    // more while a CTA stages the activations of more than 128 slices of tokens.
+    // Staging one takes about 60 instructions of a warp, as much as 1.5 chunks'
+    // products of a tile; a cluster's barriers take 1 to 2 us.  Measured (MXFP4,
+    // bf16, us with clusters of 1, 2, 4): 8 tokens x 4096 x 4096 8.4, 8.5, 8.7
+    // (128 slices); 8 x 4096 x 14336 22, 19, 16 (448); 1 x 4096 x 4096 6.0, 7.1,
+    // 7.9 (16).
+    uint32_t size = 0, clusters = 1;
+    for (uint32_t c = 1; c <= 8 && p.parts % c == 0; c *= 2) {
+        const uint32_t n = std::min(p.tiles, max_clusters(kern, c, sms));
+        if (n == 0) continue;
+        const uint32_t w = ceil_div(p.tiles, n) * (p.parts / c);
+        if (p.parts > 1 && (w > MAX_WARPS || S::smem(w, p.tile, p.parts / c) > SMEM_MAX)) continue;
+        if (size >= idle && p.tile * p.slices <= 128 * size) break;
+        size = c;
+        clusters = n;
+    }
+    if (size == 0) return cudaErrorInvalidConfiguration;
+    p.share = p.parts / size;
+    p.size_log = size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : 3;
+    p.each = p.tiles / clusters;
+    p.extra = p.tiles % clusters;
+    const uint32_t each = ceil_div(p.tiles, clusters);             // tiles of a cluster, at most
+    p.passes = p.parts > 1 ? 1 : ceil_div(each, MAX_WARPS);
+    p.lanes = ceil_div(each, p.passes);
+    p.lanes_inv = p.lanes == 1 ? 0 : static_cast<uint32_t>(((1ull << 32) + p.lanes - 1) / p.lanes);
+    p.share_inv = p.share == 1 ? 0 : static_cast<uint32_t>(((1ull << 32) + p.share - 1) / p.share);
+    const uint32_t warps = p.lanes * p.share;
+    // as many steps' activations at a time as fit, in windows of about the same size
     uint32_t windows = 1;
-    for (p.window = p.steps; p.window > 1 && S::smem(warps, p.tile, p.window * p.parts) > SMEM_MAX;
-         p.window = (p.steps + windows - 1) / windows)
+    for (p.window = p.steps; p.window > 1 && S::smem(warps, p.tile, p.window * p.share) > SMEM_MAX;
+         p.window = ceil_div(p.steps, windows))
         ++windows;
-    kern<<<dim3(grid, (p.tokens + 8 * NT - 1) / (8 * NT)), 32 * warps, S::smem(warps, p.tile, p.window * p.parts), st>>>(p);
-    return cudaGetLastError();
+    if (S::smem(warps, p.tile, p.window * p.share) > SMEM_MAX) return cudaErrorInvalidConfiguration;
+
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(clusters * size, ceil_div(p.tokens, 8 * NT));
+    cfg.blockDim = dim3(32 * warps);
+    cfg.dynamicSmemBytes = S::smem(warps, p.tile, p.window * p.share);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = size > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kern, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace mxgemv
