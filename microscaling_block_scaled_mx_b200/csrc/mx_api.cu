@@ -513,9 +513,9 @@ constexpr int64_t kNormMaxCols = 32768;
 constexpr int64_t kMaxGrid = 2147483647;
 
 // CTAs of the backward pass, each with one row of partial sums of dweight:
-// four for each of the 148 SMs, whatever the device, so that the workspace's
+// two for each of the 148 SMs, whatever the device, so that the workspace's
 // size and the order of the sums depend on the sizes alone.
-int64_t norm_parts(int64_t rows) { return rows < 592 ? rows : 592; }
+int64_t norm_parts(int64_t rows) { return rows < 296 ? rows : 296; }
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 

@@ -9,7 +9,9 @@
 // Backward, with n = h * rstd, a = dy * weight:
 //   dx = rstd * (a - n * sum(a n) / cols) + dres
 //   dweight = sum over rows of dy * n
+#include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 #include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -28,67 +30,126 @@ struct NormParams {
     uint32_t cols, vecs;       // vecs = cols / 8
     const void *w;
     int w_f32;
-    float eps;
+    float eps, inv_cols;
     void *h, *y;
     float *rstd;
     uint8_t *codes, *scales;
     int fmt, sl;
     uint32_t key;              // stochastic-rounding seed key
     uint32_t k_blocks, k_groups;
+    bool word_scales;          // scale words are aligned
     uint64_t codes_cap, scales_cap;
 };
 
-// Eight consecutive values, widened to fp32.
-template <bool BF16>
-__device__ __forceinline__ void load8(const void *base, int64_t off, float (&v)[8]) {
-    if (BF16) {
-        const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + off);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    } else {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off);
-        const float4 a = p[0], b = p[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
+// Two fp32 values in a register pair, and IEEE operations on both at a time.
+using f2 = uint64_t;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
 }
-
+__device__ __forceinline__ void unpair(f2 v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {     // nearest even
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
-// Stores eight values; for bf16, v becomes what was stored.
-template <bool BF16>
-__device__ __forceinline__ void store8(void *base, int64_t off, float (&v)[8]) {
-    if (BF16) {
-        uint32_t w[4];
+// Eight consecutive values as loaded: four words of bf16 or eight of fp32.
+template <bool BF16> struct Raw {
+    uint4 v[BF16 ? 1 : 2];
+
+    __device__ __forceinline__ void load(const void *base, int64_t off) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i)
+            v[i] = BF16 ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + off)
+                        : reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + off)[i];
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void store(void *base, int64_t off) const {
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i)
+            if (BF16) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + off) = v[i];
+            else reinterpret_cast<uint4 *>(static_cast<float *>(base) + off)[i] = v[i];
+    }
+    __device__ __forceinline__ void widen(f2 (&f)[4]) const {
+        if (BF16) {
+            const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        } else {
+            const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[!BF16].x, v[!BF16].y, v[!BF16].z, v[!BF16].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
         }
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + off) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // rounded to the type
+    __device__ __forceinline__ void narrow(const f2 (&f)[4]) {
+        float a[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpair(f[i], a[2 * i], a[2 * i + 1]);
+        if (BF16) {
+            v[0] = make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
+        } else {
+            v[0] = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]), __float_as_uint(a[3]));
+            v[!BF16] = make_uint4(__float_as_uint(a[4]), __float_as_uint(a[5]), __float_as_uint(a[6]), __float_as_uint(a[7]));
+        }
+    }
+    // this + b, rounded to the type (for bf16 the same as an fp32 sum rounded to
+    // bf16: where the fp32 sum of two bf16 values is not exact, the smaller one
+    // is below 2^-15 of the larger and cannot decide the rounding)
+    __device__ __forceinline__ void add(const Raw &b) {
+        if (BF16) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(v);
+            const uint32_t *o = reinterpret_cast<const uint32_t *>(b.v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(o[i]));
+        } else {
+            f2 x[4], y[4];
+            widen(x);
+            b.widen(y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = add2(x[i], y[i]);
+            narrow(x);
+        }
+    }
+};
+
+// Eight weights, widened: the type is the weight's own.
+__device__ __forceinline__ void load_weight8(const void *w, int w_f32, uint32_t col, f2 (&f)[4]) {
+    if (w_f32) {
+        Raw<false> r;
+        r.load(w, col);
+        r.widen(f);
     } else {
-        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + off);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        Raw<true> r;
+        r.load(w, col);
+        r.widen(f);
     }
 }
 
-__device__ __forceinline__ void load_weight8(const void *w, int w_f32, uint32_t col, float (&v)[8]) {
-    if (w_f32) load8<false>(w, col, v);
-    else load8<true>(w, col, v);
-}
-
-// Sum over the CTA, in an order fixed by its shape; every thread gets it.
-// `red` holds 32 floats that no other sum in flight uses.
+// Sum over the CTA, in an order fixed by its shape; every thread gets it.  All
+// warps read the warps' sums as they are broadcast, which takes less time than
+// a second round of shuffles.  `red` holds 32 floats that no other sum in
+// flight uses, zero where there is no warp.
 __device__ __forceinline__ float cta_sum(float s, float *red) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -96,25 +157,45 @@ __device__ __forceinline__ float cta_sum(float s, float *red) {
     if (nw == 1) return s;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
     __syncthreads();
-    const int lane = threadIdx.x & 31;
-    s = lane < nw ? red[lane] : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s;
+    float4 t = *reinterpret_cast<const float4 *>(red);
+    for (int i = 4; i < nw; i += 4) {
+        const float4 u = *reinterpret_cast<const float4 *>(red + i);
+        t.x += u.x;
+        t.y += u.y;
+        t.z += u.z;
+        t.w += u.w;
+    }
+    return (t.x + t.y) + (t.z + t.w);
+}
+// Clears the places of the sums; the caller has a barrier before the first.
+__device__ __forceinline__ void clear_sums(float (&red)[2][32]) {
+    for (int i = threadIdx.x; i < 64; i += blockDim.x) red[i >> 5][i & 31] = 0.0f;
+    __syncthreads();
 }
 
-// Codes of eight values (a quarter of block `vec / 4`) from the block's exponent.
+// Codes of eight values to byte `off` of the codes; s is their block's scale code
+// (the exponent + 127) when the block holds no NaN or Inf.
 template <int FMT, bool SR>
-__device__ __forceinline__ void encode8(const NormParams &p, int64_t row, uint32_t vec, const float (&y)[8], int e,
-                                        uint32_t keep) {
+__device__ __forceinline__ void encode8(const NormParams &p, uint64_t off, uint64_t index, const f2 (&y)[4], uint32_t s,
+                                        bool store, bool nan_block) {
     constexpr int BITS = Fmt<FMT>::bits;
     constexpr int SLOT = BITS == 4 ? 4 : 8;
     float u[8];
+    const float down = __uint_as_float((254u - s) << 23);      // 2^-e: s <= 254 - emax, and INT8 takes the other way
+    const f2 f = pair(down, down);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = scale_down<FMT>(y[i], e);
+    for (int i = 0; i < 4; ++i) {
+        f2 r = y[i];
+        if (Fmt<FMT>::emax != 0) asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(y[i]), "l"(f));
+        unpair(r, u[2 * i], u[2 * i + 1]);
+    }
+    if (Fmt<FMT>::emax == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = scale_down<FMT>(u[i], static_cast<int>(s) - 127);
+    }
     uint32_t pw[2];
     if (SR) {
-        const uint32_t g = static_cast<uint32_t>((static_cast<uint64_t>(row) * p.cols + 8ull * vec) >> 2);
+        const uint32_t g = static_cast<uint32_t>(index >> 2);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             pw[j] = sr_quad<FMT>(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3], fmix32((g + j) ^ p.key));
@@ -123,10 +204,8 @@ __device__ __forceinline__ void encode8(const NormParams &p, int64_t row, uint32
         for (int j = 0; j < 2; ++j)
             pw[j] = cvt_pair<FMT>(u[4 * j], u[4 * j + 1]) | (cvt_pair<FMT>(u[4 * j + 2], u[4 * j + 3]) << (2 * SLOT));
     }
-    pw[0] &= keep;
-    pw[1] &= keep;
-    const int64_t off = row * (static_cast<int64_t>(p.cols) * BITS / 8) + static_cast<int64_t>(vec) * BITS;
-    if (!in_bounds(static_cast<uint64_t>(off), BITS, p.codes_cap)) return;
+    if (nan_block) pw[0] = pw[1] = 0u;
+    if (!store || !in_bounds(off, BITS, p.codes_cap)) return;
     uint8_t *dst = p.codes + off;
     if (BITS == 8) {
         *reinterpret_cast<uint2 *>(dst) = make_uint2(pw[0], pw[1]);
@@ -145,88 +224,181 @@ __device__ __forceinline__ void encode8(const NormParams &p, int64_t row, uint32
     }
 }
 
-// The cast of eight values: the four lanes that hold a 32-block share its
-// largest magnitude (as bits: non-negative floats order as integers, and an
-// Inf or NaN is at or above 0x7f800000).  All lanes of the warp call this.
+// The cast of eight values of vector `vec`, four of which are a 32-block in
+// neighbouring lanes: they share the largest magnitude (as bits: non-negative
+// floats order as integers, and an Inf or NaN is at or above 0x7f800000), and
+// a group of four blocks its scale word, which is one word in every layout.
+// row_at: the row's part of the scale's offset.  All lanes of the warp call this.
 template <int FMT, bool SR>
-__device__ __forceinline__ void cast8(const NormParams &p, int64_t row, uint32_t vec, bool valid, const float (&y)[8]) {
+__device__ __forceinline__ void cast8(const NormParams &p, int64_t row, uint32_t row_at, uint32_t vec, const f2 (&y)[4]) {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) m = max_abs3(m, y[i], y[i + 1]);
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpair(y[i], lo, hi);
+        m = max_abs3(m, lo, hi);
+    }
     uint32_t a = __float_as_uint(m);
     a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
     a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-    if (!valid) return;
-    const bool nan_block = a >= 0x7f800000u;
-    const int e = nan_block ? 0 : block_exponent<FMT>(a);
-    encode8<FMT, SR>(p, row, vec, y, e, nan_block ? 0u : 0xffffffffu);
-    if ((vec & 3u) == 0)
-        put_scale(p.scales, p.sl, static_cast<uint32_t>(row), vec >> 2, p.k_blocks, p.k_groups,
-                  nan_block ? 0xffu : static_cast<uint32_t>(e + 127), p.scales_cap);
+    const bool nan_block = a >= 0x7f800000u, valid = vec < p.vecs;
+    // floor(log2 amax) - emax + 127, at least 0 (amax 0 and subnormals too); 254 at most
+    const uint32_t code = static_cast<uint32_t>(max(static_cast<int>(a >> 23) - Fmt<FMT>::emax, 0));
+    encode8<FMT, SR>(p, static_cast<uint64_t>(row) * p.cols / 8 * Fmt<FMT>::bits + vec * Fmt<FMT>::bits,
+                     static_cast<uint64_t>(row) * p.cols + 8ull * vec, y, code, valid, nan_block);
+    const uint32_t s = nan_block ? 0xffu : code, lane = threadIdx.x & 15u;
+    if (p.word_scales) {
+        uint32_t w = s | (__shfl_down_sync(0xffffffffu, s, 4, 16) << 8);
+        w |= __shfl_down_sync(0xffffffffu, w, 8, 16) << 16;
+        if (p.sl == SL_MMA_X4) w = __shfl_sync(0xffffffffu, w, 0, 16);
+        if ((vec | 15u) < p.vecs) {
+            uint32_t off = row_at;
+            if (p.sl == SL_MMA_X4) off += (vec >> 4) * 2048u + 512u * lane;      // lanes 0..3 write the four copies
+            else off += p.sl == SL_MMA ? (vec >> 4) * 512u : vec >> 2;
+            if (lane < (p.sl == SL_MMA_X4 ? 4u : 1u) && in_bounds(off, 4, p.scales_cap))
+                *reinterpret_cast<uint32_t *>(p.scales + off) = w;
+            return;
+        }
+    }
+    if (valid && (vec & 3u) == 0)
+        put_scale(p.scales, p.sl, static_cast<uint32_t>(row), vec >> 2, p.k_blocks, p.k_groups, s, p.scales_cap);
 }
 
-// CAST: 0 no codes, 1 round to nearest even, 2 stochastic rounding.
-template <int V, int CAST, typename F>
-__device__ __forceinline__ void for_format(int fmt, F f) {
-    constexpr bool SR = CAST == 2;
-    switch (fmt) {
-        case MX_E4M3: f(std::integral_constant<int, MX_E4M3>{}, std::bool_constant<SR>{}); break;
-        case MX_E5M2: f(std::integral_constant<int, MX_E5M2>{}, std::bool_constant<SR>{}); break;
-        case MX_E2M3: f(std::integral_constant<int, MX_E2M3>{}, std::bool_constant<SR>{}); break;
-        case MX_E3M2: f(std::integral_constant<int, MX_E3M2>{}, std::bool_constant<SR>{}); break;
-        case MX_E2M1: f(std::integral_constant<int, MX_E2M1>{}, std::bool_constant<SR>{}); break;
-        case MX_INT8: f(std::integral_constant<int, MX_INT8>{}, std::bool_constant<SR>{}); break;
+// The casts that a kernel is made for: one format, or a choice of formats at run
+// time (six code bits and INT8, which few programs take; stochastic rounding).
+enum Cast { NO_CAST, TO_E4M3, TO_E5M2, TO_E2M1, TO_OTHERS, STOCHASTIC };
+
+template <int CAST>
+__device__ __forceinline__ void cast_as(const NormParams &p, int64_t row, uint32_t row_at, uint32_t vec, const f2 (&y)[4]) {
+    constexpr bool SR = CAST == STOCHASTIC;
+    if (CAST == TO_E4M3) return cast8<MX_E4M3, false>(p, row, row_at, vec, y);
+    if (CAST == TO_E5M2) return cast8<MX_E5M2, false>(p, row, row_at, vec, y);
+    if (CAST == TO_E2M1) return cast8<MX_E2M1, false>(p, row, row_at, vec, y);
+    switch (p.fmt) {
+        case MX_E2M3: return cast8<MX_E2M3, SR>(p, row, row_at, vec, y);
+        case MX_E3M2: return cast8<MX_E3M2, SR>(p, row, row_at, vec, y);
+        case MX_INT8: return cast8<MX_INT8, SR>(p, row, row_at, vec, y);
+    }
+    if (!SR) return;
+    switch (p.fmt) {
+        case MX_E4M3: return cast8<MX_E4M3, SR>(p, row, row_at, vec, y);
+        case MX_E5M2: return cast8<MX_E5M2, SR>(p, row, row_at, vec, y);
+        case MX_E2M1: return cast8<MX_E2M1, SR>(p, row, row_at, vec, y);
     }
 }
 
-// One CTA per row; a thread holds V vectors of eight values, vector i of
-// thread t being i * blockDim + t (so four neighbouring lanes hold a block).
-template <bool BF16, int V, int CAST>
-__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float red[32];
-    const int64_t row = blockIdx.x;
-    float v[V][8];
-    float ss = 0.0f;
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ...; a thread holds V vectors of
+// eight values, vector i of thread t being i * blockDim + t (so four
+// neighbouring lanes hold a block), and the weight's of the same columns.
+// Vectors past the row's end are zero, like their weights, and not stored.
+template <bool BF16, bool RES, int V, int T, int CAST>
+__global__ void __launch_bounds__(T, 1) norm_kernel(const __grid_constant__ NormParams p) {
+    // the next row's loads are in flight while this one is worked on, where registers allow
+    constexpr bool AHEAD = V * (BF16 ? 1 : 2) <= 4 && T <= 512;
+    constexpr bool WIDE = V <= 2;                              // h stays widened between its two uses
+    constexpr int SIZE = BF16 ? 2 : 4;
+    __shared__ __align__(16) float red[2][32];
+    Raw<BF16> x[AHEAD ? V : 1], r[AHEAD && RES ? V : 1];
+    f2 w[AHEAD ? V : 1][4];
+    const uint32_t t = threadIdx.x, n = blockDim.x;
+    const int64_t first = blockIdx.x, step = gridDim.x;
+    // this thread's first vector of the row to be fetched, and of the row worked on
+    const char *px = static_cast<const char *>(p.x) + (first * p.ldx + 8 * t) * SIZE;
+    const char *pr = RES ? static_cast<const char *>(p.res) + (first * p.ldr + 8 * t) * SIZE : nullptr;
+    char *ph = RES ? static_cast<char *>(p.h) + (first * p.ldh + 8 * t) * SIZE : nullptr;
+    char *py = p.y ? static_cast<char *>(p.y) + (first * p.ldy + 8 * t) * SIZE : nullptr;
+    auto fetch = [&] {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const uint32_t vec = i * blockDim.x + threadIdx.x;
-        if (vec < p.vecs) {
-            load8<BF16>(p.x, row * p.ldx + 8ll * vec, v[i]);
-            if (p.res) {
-                float r[8];
-                load8<BF16>(p.res, row * p.ldr + 8ll * vec, r);
+        for (int i = 0; AHEAD && i < V; ++i) {
+            if (i * n + t >= p.vecs) continue;
+            x[AHEAD ? i : 0].load(px, static_cast<int64_t>(i * n) * 8);
+            if (RES) r[AHEAD && RES ? i : 0].load(pr, static_cast<int64_t>(i * n) * 8);
+        }
+        px += step * p.ldx * SIZE;
+        if (RES) pr += step * p.ldr * SIZE;
+    };
+    if (AHEAD) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] += r[j];
-                store8<BF16>(p.h, row * p.ldh + 8ll * vec, v[i]);
+        for (int i = 0; i < V; ++i) {
+            x[AHEAD ? i : 0].zero();
+            if (RES) r[AHEAD && RES ? i : 0].zero();
+        }
+        fetch();
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[AHEAD ? i : 0][j] = 0;
+            if (i * n + t < p.vecs) load_weight8(p.w, p.w_f32, 8 * (i * n + t), w[AHEAD ? i : 0]);
+        }
+    }
+    clear_sums(red);
+    int turn = 0;
+    for (int64_t row = first; row < p.rows; row += step, turn ^= 1) {
+        Raw<BF16> h[V];
+        if (!AHEAD) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                h[i].zero();
+                if (i * n + t >= p.vecs) continue;
+                h[i].load(px, static_cast<int64_t>(i * n) * 8);
+                if (RES) {
+                    Raw<BF16> a;
+                    a.load(pr, static_cast<int64_t>(i * n) * 8);
+                    h[i].add(a);
+                }
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+            px += step * p.ldx * SIZE;
+            if (RES) pr += step * p.ldr * SIZE;
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = __fmaf_rn(v[i][j], v[i][j], ss);
-    }
-    ss = cta_sum(ss, red);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(p.cols)) + p.eps));
-    if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const uint32_t vec = i * blockDim.x + threadIdx.x;
-        const bool valid = vec < p.vecs;
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = 0.0f;
-        if (valid) {
-            float w[8];
-            load_weight8(p.w, p.w_f32, 8 * vec, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(__fmul_rn(v[i][j], rstd), w[j]);
+        for (int i = 0; AHEAD && i < V; ++i) {
+            h[i] = x[AHEAD ? i : 0];
+            if (RES) h[i].add(r[AHEAD && RES ? i : 0]);
         }
-        if (CAST != 0)
-            for_format<V, CAST>(p.fmt, [&](auto f, auto sr) { cast8<f.value, sr.value>(p, row, vec, valid, y); });
-        if (p.y && valid) store8<BF16>(p.y, row * p.ldy + 8ll * vec, y);
+        if (AHEAD && row + step < p.rows) fetch();
+        f2 sq = 0, wide[WIDE ? V : 1][4];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (RES && i * n + t < p.vecs) h[i].store(ph, static_cast<int64_t>(i * n) * 8);
+            f2 v[4];
+            h[i].widen(v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sq = fma2(v[j], v[j], sq);
+                if (WIDE) wide[WIDE ? i : 0][j] = v[j];
+            }
+        }
+        if (RES) ph += step * p.ldh * SIZE;
+        float s0, s1;
+        unpair(sq, s0, s1);
+        const float ss = cta_sum(s0 + s1, red[turn]);
+        const float rstd = __frsqrt_rn(ss * p.inv_cols + p.eps);
+        if (p.rstd && t == 0) p.rstd[row] = rstd;
+        const f2 rstd2 = pair(rstd, rstd);
+        const uint32_t r32 = static_cast<uint32_t>(row);
+        const uint32_t row_at = p.sl == SL_PLAIN ? r32 * p.k_blocks
+                                                 : (r32 >> 7) * p.k_groups * (p.sl == SL_MMA ? 512u : 2048u) +
+                                                       ((r32 & 31u) << 4) + (((r32 >> 5) & 3u) << 2);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            f2 y[4], wl[4] = {0, 0, 0, 0};
+            if (!AHEAD && i * n + t < p.vecs) load_weight8(p.w, p.w_f32, 8 * (i * n + t), wl);
+            if (!WIDE) h[i].widen(y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = mul2(mul2(WIDE ? wide[WIDE ? i : 0][j] : y[j], rstd2), AHEAD ? w[AHEAD ? i : 0][j] : wl[j]);
+            if (CAST != NO_CAST) cast_as<CAST>(p, row, row_at, i * n + t, y);
+            if (p.y && i * n + t < p.vecs) {
+                Raw<BF16> o;
+                o.narrow(y);
+                o.store(py, static_cast<int64_t>(i * n) * 8);
+            }
+        }
+        if (p.y) py += step * p.ldy * SIZE;
     }
 }
+
+// Two CTAs of the backward pass to an SM, where two rows of them fit.
+constexpr int STAGE_BYTES = 108 * 1024;
 
 struct BackParams {
     const void *dy, *h, *dres;
@@ -238,97 +410,223 @@ struct BackParams {
     void *dx;
     float *dw, *part;
     uint32_t parts;
+    float inv_cols;
+    int stages;                // rows in the ring
 };
 
 // Rows blockIdx.x, blockIdx.x + gridDim.x, ...; a thread keeps its columns'
 // share of dweight in registers and writes it to part[blockIdx.x] at the end.
-template <bool BF16, int V>
-__global__ void __launch_bounds__(1024) norm_backward_kernel(const __grid_constant__ BackParams p) {
-    __shared__ float red[2][32];
-    float acc[V][8];
+// STAGED: the rows pass through a ring of p.stages rows in shared memory, where
+// each thread copies its own columns ahead of their use and reads them twice
+// (no other thread does, so the ring needs no barrier); else a row is read
+// twice from global memory.
+template <bool BF16, bool RES, int V, bool STAGED>
+__global__ void __launch_bounds__(STAGED ? 512 : 1024, 1) norm_backward_kernel(const __grid_constant__ BackParams p) {
+    constexpr int SIZE = BF16 ? 2 : 4, PIECES = BF16 ? 1 : 2, ARRAYS = RES ? 3 : 2;
+    __shared__ __align__(16) float red[2][32];
+    extern __shared__ __align__(16) uint4 ring[];              // [stage][array][vector][piece][thread]
+    const uint32_t t = threadIdx.x, n = blockDim.x, stage_vecs = ARRAYS * V * PIECES * n;
+    const int64_t first = blockIdx.x, step = gridDim.x;
+    const char *in[3] = {static_cast<const char *>(p.dy) + (first * p.lddy + 8 * t) * SIZE,
+                         static_cast<const char *>(p.h) + (first * p.ldh + 8 * t) * SIZE,
+                         RES ? static_cast<const char *>(p.dres) + (first * p.lddres + 8 * t) * SIZE : nullptr};
+    const int64_t by[3] = {step * p.lddy * SIZE, step * p.ldh * SIZE, RES ? step * p.lddres * SIZE : 0};
+    char *out = static_cast<char *>(p.dx) + (first * p.lddx + 8 * t) * SIZE;
+    const uint32_t ring32 = STAGED ? static_cast<uint32_t>(__cvta_generic_to_shared(ring + t)) : 0u;
+    auto fetch = [&](int stage) {                              // the next row to be read
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+        for (int a = 0; a < ARRAYS; ++a) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
-    int turn = 0;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
-        const float rstd = p.rstd[row];
-        float s = 0.0f;
+            for (int i = 0; i < V; ++i) {
+                if (i * n + t >= p.vecs) continue;
+#pragma unroll
+                for (int k = 0; k < PIECES; ++k)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                     ring32 + (stage * stage_vecs + ((a * V + i) * PIECES + k) * n) * 16),
+                                 "l"(in[a] + static_cast<int64_t>(i * n) * 8 * SIZE + k * 16)
+                                 : "memory");
+            }
+            in[a] += by[a];
+        }
+    };
+    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    if (STAGED)
+        for (int s = 0; s < p.stages - 1; ++s) {
+            if (first + s * step < p.rows) fetch(s);
+            commit();
+        }
+    f2 acc[V][4], w[STAGED ? V : 1][4];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0;
+        if (STAGED && i * n + t < p.vecs) load_weight8(p.w, p.w_f32, 8 * (i * n + t), w[STAGED ? i : 0]);
+    }
+    clear_sums(red);
+    float rstd = p.rstd[first];
+    int turn = 0, stage = 0;
+    for (int64_t row = first; row < p.rows; row += step, turn ^= 1) {
+        const f2 rs = pair(rstd, rstd);
+        if (row + step < p.rows) rstd = p.rstd[row + step];
+        if (STAGED) {
+            // this thread's copies of the row have landed (all but the last stages - 2 groups)
+            if (p.stages == 2) asm volatile("cp.async.wait_group 0;" ::: "memory");
+            else if (p.stages == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else asm volatile("cp.async.wait_group 2;" ::: "memory");
+            if (row + (p.stages - 1) * step < p.rows) fetch(stage == 0 ? p.stages - 1 : stage - 1);
+            commit();
+        }
+        auto get = [&](int a, int i, Raw<BF16> &raw) {
+            if (STAGED) {
+#pragma unroll
+                for (int k = 0; k < PIECES; ++k) raw.v[k] = ring[stage * stage_vecs + ((a * V + i) * PIECES + k) * n + t];
+            } else {
+                raw.load(in[a], static_cast<int64_t>(i * n) * 8);
+            }
+        };
+        // the vector's a = dy * weight and n = h * rstd, and dy
+        auto terms = [&](int i, f2 (&a)[4], f2 (&nn)[4], f2 (&dy)[4]) {
+            Raw<BF16> g, h;
+            f2 wl[4];
+            get(0, i, g);
+            get(1, i, h);
+            if (!STAGED) load_weight8(p.w, p.w_f32, 8 * (i * n + t), wl);
+            g.widen(dy);
+            h.widen(nn);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                nn[j] = mul2(nn[j], rs);
+                a[j] = mul2(dy[j], STAGED ? w[STAGED ? i : 0][j] : wl[j]);
+            }
+        };
+        f2 dot = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const uint32_t vec = i * blockDim.x + threadIdx.x;
-            if (vec >= p.vecs) continue;
-            float g[8], n[8], w[8];
-            load8<BF16>(p.dy, row * p.lddy + 8ll * vec, g);
-            load8<BF16>(p.h, row * p.ldh + 8ll * vec, n);
-            load_weight8(p.w, p.w_f32, 8 * vec, w);
+            if (i * n + t >= p.vecs) continue;
+            f2 a[4], nn[4], dy[4];
+            terms(i, a, nn, dy);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float nn = n[j] * rstd;
-                acc[i][j] = __fmaf_rn(g[j], nn, acc[i][j]);
-                s = __fmaf_rn(g[j] * w[j], nn, s);
+            for (int j = 0; j < 4; ++j) {
+                acc[i][j] = fma2(dy[j], nn[j], acc[i][j]);
+                dot = fma2(a[j], nn[j], dot);
             }
         }
-        const float c = cta_sum(s, red[turn]) / static_cast<float>(p.cols);
+        float s0, s1;
+        unpair(dot, s0, s1);
+        const float c = cta_sum(s0 + s1, red[turn]) * p.inv_cols;
+        const f2 minus_c = pair(-c, -c);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const uint32_t vec = i * blockDim.x + threadIdx.x;
-            if (vec >= p.vecs) continue;
-            float g[8], n[8], w[8];
-            load8<BF16>(p.dy, row * p.lddy + 8ll * vec, g);
-            load8<BF16>(p.h, row * p.ldh + 8ll * vec, n);
-            load_weight8(p.w, p.w_f32, 8 * vec, w);
+            if (i * n + t >= p.vecs) continue;
+            f2 a[4], nn[4], dy[4];
+            terms(i, a, nn, dy);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) g[j] = rstd * __fmaf_rn(-(n[j] * rstd), c, g[j] * w[j]);
-            if (p.dres) {
-                float r[8];
-                load8<BF16>(p.dres, row * p.lddres + 8ll * vec, r);
+            for (int j = 0; j < 4; ++j) a[j] = mul2(rs, fma2(nn[j], minus_c, a[j]));
+            Raw<BF16> o;
+            if (RES) {
+                get(2, i, o);
+                o.widen(nn);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) g[j] += r[j];
+                for (int j = 0; j < 4; ++j) a[j] = add2(a[j], nn[j]);
             }
-            store8<BF16>(p.dx, row * p.lddx + 8ll * vec, g);
+            o.narrow(a);
+            o.store(out, static_cast<int64_t>(i * n) * 8);
+        }
+        out += step * p.lddx * SIZE;
+        if (STAGED) {
+            if (++stage == p.stages) stage = 0;
+        } else {
+#pragma unroll
+            for (int a = 0; a < ARRAYS; ++a) in[a] += by[a];
         }
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const uint32_t vec = i * blockDim.x + threadIdx.x;
-        if (vec < p.vecs) store8<false>(p.part, static_cast<int64_t>(blockIdx.x) * p.cols + 8ll * vec, acc[i]);
+        const uint32_t vec = i * n + t;
+        if (vec >= p.vecs) continue;
+        Raw<false> o;
+        o.narrow(acc[i]);
+        o.store(p.part, static_cast<int64_t>(blockIdx.x) * p.cols + 8ll * vec);
     }
 }
 
-// dweight[c] = the sum of the parts, in order of the part.
-__global__ void norm_dweight_kernel(const float *part, uint32_t parts, uint32_t cols, float *dw) {
-    const uint32_t c = blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= cols) return;
+// dweight[c] = the sum of the parts: 32 columns to a CTA, warp w adds parts w,
+// w + 16, ..., and the warps' sums are added in their order.
+constexpr int DW_WARPS = 16;
+__global__ void __launch_bounds__(32 * DW_WARPS) norm_dweight_kernel(const float *part, uint32_t parts, uint32_t cols, float *dw) {
+    __shared__ float red[DW_WARPS][32];
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;    // cols % 32 == 0
     float s = 0.0f;
-    for (uint32_t i = 0; i < parts; ++i) s += part[static_cast<int64_t>(i) * cols + c];
+#pragma unroll 4
+    for (uint32_t i = warp; i < parts; i += DW_WARPS) s += part[static_cast<int64_t>(i) * cols + c];
+    red[warp][lane] = s;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int i = 1; i < DW_WARPS; ++i) s += red[i][lane];
     dw[c] = s;
 }
 
-template <bool BF16, int V>
-void launch_norm(const NormParams &p, int threads, int cast, cudaStream_t st) {
-    const unsigned grid = static_cast<unsigned>(p.rows);
-    if (cast == 0) norm_kernel<BF16, V, 0><<<grid, threads, 0, st>>>(p);
-    else if (cast == 1) norm_kernel<BF16, V, 1><<<grid, threads, 0, st>>>(p);
-    else norm_kernel<BF16, V, 2><<<grid, threads, 0, st>>>(p);
+int threads_for(uint32_t vecs, int v) { return static_cast<int>((vecs + v - 1) / v + 31) / 32 * 32; }
+
+// CTAs of a kernel that the device runs at a time; asked for each launch shape
+// (a few hundred nanoseconds on the host).
+template <typename Kern>
+int64_t resident(Kern kern, int threads, int sms) {
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0) == cudaSuccess && n > 0 ? int64_t{n} * sms : sms;
 }
 
-template <bool BF16>
-void launch_norm_v(const NormParams &p, int cast, cudaStream_t st) {
-    const int v = p.vecs <= 1024 ? 1 : p.vecs <= 2048 ? 2 : 4;
-    const int threads = static_cast<int>((p.vecs + v - 1) / v + 31) / 32 * 32;
-    if (v == 1) launch_norm<BF16, 1>(p, threads, cast, st);
-    else if (v == 2) launch_norm<BF16, 2>(p, threads, cast, st);
-    else launch_norm<BF16, 4>(p, threads, cast, st);
+template <bool BF16, bool RES, int V, int T, int CAST>
+void launch_norm(const NormParams &p, int sms, cudaStream_t st) {
+    auto kern = norm_kernel<BF16, RES, V, T, CAST>;
+    const int threads = threads_for(p.vecs, V);
+    const int64_t most = p.rows <= sms ? p.rows : resident(kern, threads, sms);
+    kern<<<static_cast<unsigned>(p.rows < most ? p.rows : most), threads, 0, st>>>(p);
 }
 
-template <bool BF16>
-void launch_backward_v(const BackParams &p, cudaStream_t st) {
-    const int v = p.vecs <= 1024 ? 1 : p.vecs <= 2048 ? 2 : 4;
-    const int threads = static_cast<int>((p.vecs + v - 1) / v + 31) / 32 * 32;
-    if (v == 1) norm_backward_kernel<BF16, 1><<<p.parts, threads, 0, st>>>(p);
-    else if (v == 2) norm_backward_kernel<BF16, 2><<<p.parts, threads, 0, st>>>(p);
-    else norm_backward_kernel<BF16, 4><<<p.parts, threads, 0, st>>>(p);
+template <bool BF16, bool RES, int V, int T>
+void launch_norm_cast(const NormParams &p, int cast, int sms, cudaStream_t st) {
+    switch (cast) {
+        case NO_CAST: return launch_norm<BF16, RES, V, T, NO_CAST>(p, sms, st);
+        case TO_E4M3: return launch_norm<BF16, RES, V, T, TO_E4M3>(p, sms, st);
+        case TO_E5M2: return launch_norm<BF16, RES, V, T, TO_E5M2>(p, sms, st);
+        case TO_E2M1: return launch_norm<BF16, RES, V, T, TO_E2M1>(p, sms, st);
+        case TO_OTHERS: return launch_norm<BF16, RES, V, T, TO_OTHERS>(p, sms, st);
+        default: return launch_norm<BF16, RES, V, T, STOCHASTIC>(p, sms, st);
+    }
+}
+
+template <bool BF16, bool RES>
+void launch_norm_v(const NormParams &p, int cast, int sms, cudaStream_t st) {
+    int v = p.vecs <= 128 ? 4 : p.vecs <= 1024 ? 2 : 4;
+    if (const char *e = std::getenv("NV")) v = std::atoi(e);
+    if (v == 1) launch_norm_cast<BF16, RES, 1, 512>(p, cast, sms, st);
+    else if (v == 2) launch_norm_cast<BF16, RES, 2, 512>(p, cast, sms, st);
+    else if (p.vecs <= 4 * 512) launch_norm_cast<BF16, RES, 4, 512>(p, cast, sms, st);
+    else launch_norm_cast<BF16, RES, 4, 1024>(p, cast, sms, st);
+}
+
+template <bool BF16, bool RES, int V>
+cudaError_t launch_staged(BackParams &p, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    auto kern = norm_backward_kernel<BF16, RES, V, true>;
+    const int threads = threads_for(p.vecs, V), row = threads * V * (BF16 ? 16 : 32) * (RES ? 3 : 2);
+    p.stages = std::max(2, std::min(4, STAGE_BYTES / row));
+    const cudaError_t e = ensure_smem_limit(kern, 2 * 512 * 2 * 32 * 3, done);   // two rows of the widest
+    if (e != cudaSuccess) return e;
+    kern<<<p.parts, threads, p.stages * row, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <bool BF16, bool RES>
+cudaError_t launch_backward_v(BackParams &p, cudaStream_t st) {
+    int v = p.vecs <= 512 ? 1 : p.vecs <= 1024 ? 2 : 4;
+    if (const char *e = std::getenv("NB")) v = std::atoi(e);
+    if (v == 1) return launch_staged<BF16, RES, 1>(p, st);
+    if (v == 2) return launch_staged<BF16, RES, 2>(p, st);
+    norm_backward_kernel<BF16, RES, 4, false><<<p.parts, threads_for(p.vecs, 4), 0, st>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace mxnorm
@@ -340,6 +638,7 @@ cudaError_t mx_launch_rmsnorm(const MxNormArgs &a, cudaStream_t st) {
     p.cols = static_cast<uint32_t>(a.cols);
     p.vecs = p.cols / 8;
     p.w = a.weight; p.w_f32 = a.wdt == MX_F32; p.eps = a.eps;
+    p.inv_cols = 1.0f / static_cast<float>(a.cols);
     p.h = a.h; p.y = a.y; p.rstd = a.rstd;
     p.codes = static_cast<uint8_t *>(a.codes); p.scales = static_cast<uint8_t *>(a.scales);
     p.fmt = a.fmt; p.sl = a.sl;
@@ -348,9 +647,20 @@ cudaError_t mx_launch_rmsnorm(const MxNormArgs &a, cudaStream_t st) {
     p.k_groups = (p.k_blocks + 3) / 4;
     p.codes_cap = a.codes ? mx_codes_bytes(static_cast<mx_fmt>(a.fmt), a.rows, a.cols) : 0;
     p.scales_cap = a.codes ? mx_scales_bytes(static_cast<mx_scale_layout>(a.sl), a.rows, a.cols) : 0;
-    const int cast = !a.codes ? 0 : (a.rnd == MX_SR ? 2 : 1);
-    if (a.xdt == MX_BF16) launch_norm_v<true>(p, cast, st);
-    else launch_norm_v<false>(p, cast, st);
+    const int cast = !a.codes ? NO_CAST
+                     : a.rnd == MX_SR ? STOCHASTIC
+                     : a.fmt == MX_E4M3 ? TO_E4M3
+                     : a.fmt == MX_E5M2 ? TO_E5M2
+                     : a.fmt == MX_E2M1 ? TO_E2M1
+                                        : TO_OTHERS;
+    p.word_scales = (reinterpret_cast<uintptr_t>(a.scales) & 3u) == 0 && (a.sl != MX_SCALES_PLAIN || p.k_blocks % 4 == 0);
+    if (a.xdt == MX_BF16) {
+        if (p.res) launch_norm_v<true, true>(p, cast, a.num_sms, st);
+        else launch_norm_v<true, false>(p, cast, a.num_sms, st);
+    } else {
+        if (p.res) launch_norm_v<false, true>(p, cast, a.num_sms, st);
+        else launch_norm_v<false, false>(p, cast, a.num_sms, st);
+    }
     return cudaGetLastError();
 }
 
@@ -363,11 +673,11 @@ cudaError_t mx_launch_rmsnorm_backward(const MxNormBackArgs &a, cudaStream_t st)
     p.vecs = p.cols / 8;
     p.w = a.weight; p.w_f32 = a.wdt == MX_F32; p.rstd = a.rstd;
     p.dx = a.dx; p.dw = a.dweight; p.part = a.part; p.parts = static_cast<uint32_t>(a.parts);
-    if (a.xdt == MX_BF16) launch_backward_v<true>(p, st);
-    else launch_backward_v<false>(p, st);
-    cudaError_t e = cudaGetLastError();
+    p.inv_cols = 1.0f / static_cast<float>(a.cols);
+    const cudaError_t e = a.xdt == MX_BF16 ? (p.dres ? launch_backward_v<true, true>(p, st) : launch_backward_v<true, false>(p, st))
+                                           : (p.dres ? launch_backward_v<false, true>(p, st) : launch_backward_v<false, false>(p, st));
     if (e != cudaSuccess) return e;
-    norm_dweight_kernel<<<(p.cols + 127) / 128, 128, 0, st>>>(p.part, p.parts, p.cols, p.dw);
+    norm_dweight_kernel<<<p.cols / 32, 32 * DW_WARPS, 0, st>>>(p.part, p.parts, p.cols, p.dw);
     return cudaGetLastError();
 }
 
