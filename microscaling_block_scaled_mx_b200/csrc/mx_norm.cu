@@ -11,7 +11,6 @@
 //   dweight = sum over rows of dy * n
 #include <algorithm>
 #include <cstdint>
-#include <cstdlib>
 #include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -38,6 +37,7 @@ struct NormParams {
     uint32_t key;              // stochastic-rounding seed key
     uint32_t k_blocks, k_groups;
     bool word_scales;          // scale words are aligned
+    bool wide;                 // fp32: every row starts on a 32-byte boundary
     uint64_t codes_cap, scales_cap;
 };
 
@@ -74,7 +74,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {     // neare
 template <bool BF16> struct Raw {
     uint4 v[BF16 ? 1 : 2];
 
-    __device__ __forceinline__ void load(const void *base, int64_t off) {
+    // wide: fp32 values on a 32-byte boundary, as one access (two halves would
+    // each touch every 32-byte sector of the warp's)
+    __device__ __forceinline__ void load(const void *base, int64_t off, bool wide) {
+        if (!BF16 && wide) {
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[!BF16].x), "=r"(v[!BF16].y),
+                           "=r"(v[!BF16].z), "=r"(v[!BF16].w)
+                         : "l"(static_cast<const float *>(base) + off)
+                         : "memory");
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < (BF16 ? 1 : 2); ++i)
             v[i] = BF16 ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + off)
@@ -84,7 +94,14 @@ template <bool BF16> struct Raw {
 #pragma unroll
         for (int i = 0; i < (BF16 ? 1 : 2); ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
     }
-    __device__ __forceinline__ void store(void *base, int64_t off) const {
+    __device__ __forceinline__ void store(void *base, int64_t off, bool wide) const {
+        if (!BF16 && wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<float *>(base) + off),
+                         "r"(v[0].x), "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[!BF16].x), "r"(v[!BF16].y), "r"(v[!BF16].z),
+                         "r"(v[!BF16].w)
+                         : "memory");
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < (BF16 ? 1 : 2); ++i)
             if (BF16) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + off) = v[i];
@@ -137,11 +154,11 @@ template <bool BF16> struct Raw {
 __device__ __forceinline__ void load_weight8(const void *w, int w_f32, uint32_t col, f2 (&f)[4]) {
     if (w_f32) {
         Raw<false> r;
-        r.load(w, col);
+        r.load(w, col, false);
         r.widen(f);
     } else {
         Raw<true> r;
-        r.load(w, col);
+        r.load(w, col, false);
         r.widen(f);
     }
 }
@@ -311,8 +328,8 @@ __global__ void __launch_bounds__(T, 1) norm_kernel(const __grid_constant__ Norm
 #pragma unroll
         for (int i = 0; AHEAD && i < V; ++i) {
             if (i * n + t >= p.vecs) continue;
-            x[AHEAD ? i : 0].load(px, static_cast<int64_t>(i * n) * 8);
-            if (RES) r[AHEAD && RES ? i : 0].load(pr, static_cast<int64_t>(i * n) * 8);
+            x[AHEAD ? i : 0].load(px, static_cast<int64_t>(i * n) * 8, p.wide);
+            if (RES) r[AHEAD && RES ? i : 0].load(pr, static_cast<int64_t>(i * n) * 8, p.wide);
         }
         px += step * p.ldx * SIZE;
         if (RES) pr += step * p.ldr * SIZE;
@@ -340,10 +357,10 @@ __global__ void __launch_bounds__(T, 1) norm_kernel(const __grid_constant__ Norm
             for (int i = 0; i < V; ++i) {
                 h[i].zero();
                 if (i * n + t >= p.vecs) continue;
-                h[i].load(px, static_cast<int64_t>(i * n) * 8);
+                h[i].load(px, static_cast<int64_t>(i * n) * 8, p.wide);
                 if (RES) {
                     Raw<BF16> a;
-                    a.load(pr, static_cast<int64_t>(i * n) * 8);
+                    a.load(pr, static_cast<int64_t>(i * n) * 8, p.wide);
                     h[i].add(a);
                 }
             }
@@ -359,7 +376,7 @@ __global__ void __launch_bounds__(T, 1) norm_kernel(const __grid_constant__ Norm
         f2 sq = 0, wide[WIDE ? V : 1][4];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (RES && i * n + t < p.vecs) h[i].store(ph, static_cast<int64_t>(i * n) * 8);
+            if (RES && i * n + t < p.vecs) h[i].store(ph, static_cast<int64_t>(i * n) * 8, p.wide);
             f2 v[4];
             h[i].widen(v);
 #pragma unroll
@@ -390,20 +407,17 @@ __global__ void __launch_bounds__(T, 1) norm_kernel(const __grid_constant__ Norm
             if (p.y && i * n + t < p.vecs) {
                 Raw<BF16> o;
                 o.narrow(y);
-                o.store(py, static_cast<int64_t>(i * n) * 8);
+                o.store(py, static_cast<int64_t>(i * n) * 8, p.wide);
             }
         }
         if (p.y) py += step * p.ldy * SIZE;
     }
 }
 
-// Two CTAs of the backward pass to an SM, where two rows of them fit.
-constexpr int STAGE_BYTES = 108 * 1024;
-
 struct BackParams {
     const void *dy, *h, *dres;
     int64_t rows, lddy, ldh, lddres, lddx;
-    uint32_t cols, vecs;
+    uint32_t cols, pieces;     // 16-byte pieces of a row
     const void *w;
     int w_f32;
     const float *rstd;
@@ -411,60 +425,127 @@ struct BackParams {
     float *dw, *part;
     uint32_t parts;
     float inv_cols;
-    int stages;                // rows in the ring
+    uint32_t threads, groups;  // threads to a row, rows of a CTA at a time
+    int stages;                // rows in each group's ring
 };
 
-// Rows blockIdx.x, blockIdx.x + gridDim.x, ...; a thread keeps its columns'
-// share of dweight in registers and writes it to part[blockIdx.x] at the end.
+// 16 bytes as loaded, eight bf16 values or four fp32 ones.
+template <bool BF16> struct Piece {
+    static constexpr int PAIRS = BF16 ? 4 : 2, VALUES = 2 * PAIRS;
+    uint4 v;
+
+    __device__ __forceinline__ void widen(f2 (&f)[PAIRS]) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i)
+            f[i] = BF16 ? pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u))
+                        : pair(__uint_as_float(w[2 * (i & 1)]), __uint_as_float(w[2 * (i & 1) + 1]));
+    }
+    __device__ __forceinline__ void narrow(const f2 (&f)[PAIRS]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+            float lo, hi;
+            unpair(f[i], lo, hi);
+            if (BF16) {
+                w[i] = pack_bf16(lo, hi);
+            } else {
+                w[2 * (i & 1)] = __float_as_uint(lo);
+                w[2 * (i & 1) + 1] = __float_as_uint(hi);
+            }
+        }
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // the weights of the piece's columns from `col`
+    static __device__ __forceinline__ void weights(const void *w, int w_f32, uint32_t col, f2 (&f)[PAIRS]) {
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+            if (w_f32) {
+                const float2 a = reinterpret_cast<const float2 *>(static_cast<const float *>(w) + col)[i];
+                f[i] = pair(a.x, a.y);
+            } else {
+                const uint32_t a = reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(w) + col)[i];
+                f[i] = pair(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+            }
+        }
+    }
+};
+
+// Sum over a group of `warps` warps in the fixed order of cta_sum; `barrier` is
+// the group's own, `red` its place (with room for a multiple of four).
+__device__ __forceinline__ float group_sum(float s, float *red, uint32_t warps, uint32_t warp, uint32_t barrier) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (warps == 1) return s;
+    if ((threadIdx.x & 31) == 0) red[warp] = s;
+    asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(warps * 32) : "memory");
+    float4 t = *reinterpret_cast<const float4 *>(red);
+    for (uint32_t i = 4; i < warps; i += 4) {
+        const float4 u = *reinterpret_cast<const float4 *>(red + i);
+        t.x += u.x;
+        t.y += u.y;
+        t.z += u.z;
+        t.w += u.w;
+    }
+    return (t.x + t.y) + (t.z + t.w);
+}
+
+// Group k of CTA b takes rows b * groups + k, and every gridDim * groups rows
+// from there; a thread has V pieces of a row, piece i * threads + t.  It keeps
+// its columns' share of dweight in registers; at the end the groups' shares are
+// added in order and written to part[b].
 // STAGED: the rows pass through a ring of p.stages rows in shared memory, where
 // each thread copies its own columns ahead of their use and reads them twice
 // (no other thread does, so the ring needs no barrier); else a row is read
 // twice from global memory.
 template <bool BF16, bool RES, int V, bool STAGED>
-__global__ void __launch_bounds__(STAGED ? 512 : 1024, 1) norm_backward_kernel(const __grid_constant__ BackParams p) {
-    constexpr int SIZE = BF16 ? 2 : 4, PIECES = BF16 ? 1 : 2, ARRAYS = RES ? 3 : 2;
+__global__ void __launch_bounds__(STAGED || BF16 ? 512 : 1024, 1) norm_backward_kernel(const __grid_constant__ BackParams p) {
+    using P = Piece<BF16>;
+    constexpr int ARRAYS = RES ? 3 : 2;
     __shared__ __align__(16) float red[2][32];
-    extern __shared__ __align__(16) uint4 ring[];              // [stage][array][vector][piece][thread]
-    const uint32_t t = threadIdx.x, n = blockDim.x, stage_vecs = ARRAYS * V * PIECES * n;
-    const int64_t first = blockIdx.x, step = gridDim.x;
-    const char *in[3] = {static_cast<const char *>(p.dy) + (first * p.lddy + 8 * t) * SIZE,
-                         static_cast<const char *>(p.h) + (first * p.ldh + 8 * t) * SIZE,
-                         RES ? static_cast<const char *>(p.dres) + (first * p.lddres + 8 * t) * SIZE : nullptr};
+    extern __shared__ __align__(16) uint4 ring[];              // [group][stage][array][piece]
+    const uint32_t n = p.threads, group = threadIdx.x / n, t = threadIdx.x - group * n;
+    const uint32_t warps = n / 32, warp = t >> 5, row_vecs = V * n, stage_vecs = ARRAYS * row_vecs;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * p.groups + group, step = static_cast<int64_t>(gridDim.x) * p.groups;
+    constexpr int SIZE = BF16 ? 2 : 4;
+    const char *in[3] = {static_cast<const char *>(p.dy) + first * p.lddy * SIZE + 16 * t,
+                         static_cast<const char *>(p.h) + first * p.ldh * SIZE + 16 * t,
+                         RES ? static_cast<const char *>(p.dres) + first * p.lddres * SIZE + 16 * t : nullptr};
     const int64_t by[3] = {step * p.lddy * SIZE, step * p.ldh * SIZE, RES ? step * p.lddres * SIZE : 0};
-    char *out = static_cast<char *>(p.dx) + (first * p.lddx + 8 * t) * SIZE;
-    const uint32_t ring32 = STAGED ? static_cast<uint32_t>(__cvta_generic_to_shared(ring + t)) : 0u;
-    auto fetch = [&](int stage) {                              // the next row to be read
+    char *out = static_cast<char *>(p.dx) + first * p.lddx * SIZE + 16 * t;
+    uint4 *mine = ring + group * p.stages * stage_vecs + t;
+    const uint32_t mine32 = STAGED ? static_cast<uint32_t>(__cvta_generic_to_shared(mine)) : 0u;
+    auto fetch = [&](uint32_t at) {                            // the next row to be read
 #pragma unroll
         for (int a = 0; a < ARRAYS; ++a) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (i * n + t >= p.vecs) continue;
-#pragma unroll
-                for (int k = 0; k < PIECES; ++k)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                     ring32 + (stage * stage_vecs + ((a * V + i) * PIECES + k) * n) * 16),
-                                 "l"(in[a] + static_cast<int64_t>(i * n) * 8 * SIZE + k * 16)
+            for (int i = 0; i < V; ++i)
+                if (i * n + t < p.pieces)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(mine32 + (at + a * row_vecs + i * n) * 16),
+                                 "l"(in[a] + i * n * 16)
                                  : "memory");
-            }
             in[a] += by[a];
         }
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
     if (STAGED)
         for (int s = 0; s < p.stages - 1; ++s) {
-            if (first + s * step < p.rows) fetch(s);
+            if (first + s * step < p.rows) fetch(s * stage_vecs);
             commit();
         }
-    f2 acc[V][4], w[STAGED ? V : 1][4];
+    f2 acc[V][P::PAIRS], w[STAGED ? V : 1][P::PAIRS];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0;
-        if (STAGED && i * n + t < p.vecs) load_weight8(p.w, p.w_f32, 8 * (i * n + t), w[STAGED ? i : 0]);
+        for (int j = 0; j < P::PAIRS; ++j) acc[i][j] = 0;
+        if (STAGED && i * n + t < p.pieces) P::weights(p.w, p.w_f32, (i * n + t) * P::VALUES, w[STAGED ? i : 0]);
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");      // the sum of the parts may be launched
     clear_sums(red);
-    float rstd = p.rstd[first];
-    int turn = 0, stage = 0;
+    float rstd = first < p.rows ? p.rstd[first] : 0.0f;
+    int turn = 0;
+    const uint32_t last = (p.stages - 1) * stage_vecs, place = group * ((warps + 3) & ~3u);
+    uint32_t at = 0;
     for (int64_t row = first; row < p.rows; row += step, turn ^= 1) {
         const f2 rs = pair(rstd, rstd);
         if (row + step < p.rows) rstd = p.rstd[row + step];
@@ -473,28 +554,23 @@ __global__ void __launch_bounds__(STAGED ? 512 : 1024, 1) norm_backward_kernel(c
             if (p.stages == 2) asm volatile("cp.async.wait_group 0;" ::: "memory");
             else if (p.stages == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
             else asm volatile("cp.async.wait_group 2;" ::: "memory");
-            if (row + (p.stages - 1) * step < p.rows) fetch(stage == 0 ? p.stages - 1 : stage - 1);
+            if (row + (p.stages - 1) * step < p.rows) fetch(at == 0 ? last : at - stage_vecs);
             commit();
         }
-        auto get = [&](int a, int i, Raw<BF16> &raw) {
-            if (STAGED) {
-#pragma unroll
-                for (int k = 0; k < PIECES; ++k) raw.v[k] = ring[stage * stage_vecs + ((a * V + i) * PIECES + k) * n + t];
-            } else {
-                raw.load(in[a], static_cast<int64_t>(i * n) * 8);
-            }
+        auto get = [&](int a, int i, P &x) {
+            x.v = STAGED ? mine[at + a * row_vecs + i * n] : *reinterpret_cast<const uint4 *>(in[a] + i * n * 16);
         };
-        // the vector's a = dy * weight and n = h * rstd, and dy
-        auto terms = [&](int i, f2 (&a)[4], f2 (&nn)[4], f2 (&dy)[4]) {
-            Raw<BF16> g, h;
-            f2 wl[4];
+        // the piece's a = dy * weight and n = h * rstd, and dy
+        auto terms = [&](int i, f2 (&a)[P::PAIRS], f2 (&nn)[P::PAIRS], f2 (&dy)[P::PAIRS]) {
+            P g, h;
+            f2 wl[P::PAIRS];
             get(0, i, g);
             get(1, i, h);
-            if (!STAGED) load_weight8(p.w, p.w_f32, 8 * (i * n + t), wl);
+            if (!STAGED) P::weights(p.w, p.w_f32, (i * n + t) * P::VALUES, wl);
             g.widen(dy);
             h.widen(nn);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < P::PAIRS; ++j) {
                 nn[j] = mul2(nn[j], rs);
                 a[j] = mul2(dy[j], STAGED ? w[STAGED ? i : 0][j] : wl[j]);
             }
@@ -502,62 +578,81 @@ __global__ void __launch_bounds__(STAGED ? 512 : 1024, 1) norm_backward_kernel(c
         f2 dot = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (i * n + t >= p.vecs) continue;
-            f2 a[4], nn[4], dy[4];
+            if (i * n + t >= p.pieces) continue;
+            f2 a[P::PAIRS], nn[P::PAIRS], dy[P::PAIRS];
             terms(i, a, nn, dy);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < P::PAIRS; ++j) {
                 acc[i][j] = fma2(dy[j], nn[j], acc[i][j]);
                 dot = fma2(a[j], nn[j], dot);
             }
         }
         float s0, s1;
         unpair(dot, s0, s1);
-        const float c = cta_sum(s0 + s1, red[turn]) * p.inv_cols;
+        const float c = group_sum(s0 + s1, red[turn] + place, warps, warp, 1 + group) * p.inv_cols;
         const f2 minus_c = pair(-c, -c);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (i * n + t >= p.vecs) continue;
-            f2 a[4], nn[4], dy[4];
+            if (i * n + t >= p.pieces) continue;
+            f2 a[P::PAIRS], nn[P::PAIRS], dy[P::PAIRS];
             terms(i, a, nn, dy);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) a[j] = mul2(rs, fma2(nn[j], minus_c, a[j]));
-            Raw<BF16> o;
+            for (int j = 0; j < P::PAIRS; ++j) a[j] = mul2(rs, fma2(nn[j], minus_c, a[j]));
+            P o;
             if (RES) {
                 get(2, i, o);
                 o.widen(nn);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) a[j] = add2(a[j], nn[j]);
+                for (int j = 0; j < P::PAIRS; ++j) a[j] = add2(a[j], nn[j]);
             }
             o.narrow(a);
-            o.store(out, static_cast<int64_t>(i * n) * 8);
+            *reinterpret_cast<uint4 *>(out + i * n * 16) = o.v;
         }
         out += step * p.lddx * SIZE;
         if (STAGED) {
-            if (++stage == p.stages) stage = 0;
+            at = at == last ? 0 : at + stage_vecs;
         } else {
 #pragma unroll
             for (int a = 0; a < ARRAYS; ++a) in[a] += by[a];
         }
     }
+    // the groups' shares, through the ring (its copies have landed) and in order
+    float *part = p.part + static_cast<int64_t>(blockIdx.x) * p.cols;
+    float *shares = reinterpret_cast<float *>(ring);
+    if (p.groups > 1) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const uint32_t vec = i * n + t;
-        if (vec >= p.vecs) continue;
-        Raw<false> o;
-        o.narrow(acc[i]);
-        o.store(p.part, static_cast<int64_t>(blockIdx.x) * p.cols + 8ll * vec);
+        if (i * n + t >= p.pieces) continue;
+        float *to = (p.groups > 1 ? shares + group * p.cols : part) + (i * n + t) * P::VALUES;
+#pragma unroll
+        for (int j = 0; j < P::PAIRS; ++j) {
+            float lo, hi;
+            unpair(acc[i][j], lo, hi);
+            reinterpret_cast<float2 *>(to)[j] = make_float2(lo, hi);
+        }
+    }
+    if (p.groups == 1) return;
+    __syncthreads();
+    for (uint32_t c = threadIdx.x; c < p.cols; c += blockDim.x) {
+        float s = shares[c];
+        for (uint32_t k = 1; k < p.groups; ++k) s += shares[k * p.cols + c];
+        part[c] = s;
     }
 }
 
 // dweight[c] = the sum of the parts: 32 columns to a CTA, warp w adds parts w,
-// w + 16, ..., and the warps' sums are added in their order.
-constexpr int DW_WARPS = 16;
+// w + 32, ..., and the warps' sums are added in their order.  Launched while the
+// backward kernel still runs; it waits for that kernel's end before it reads.
+constexpr int DW_WARPS = 32;
 __global__ void __launch_bounds__(32 * DW_WARPS) norm_dweight_kernel(const float *part, uint32_t parts, uint32_t cols, float *dw) {
     __shared__ float red[DW_WARPS][32];
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;    // cols % 32 == 0
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float s = 0.0f;
-#pragma unroll 4
+#pragma unroll 10
     for (uint32_t i = warp; i < parts; i += DW_WARPS) s += part[static_cast<int64_t>(i) * cols + c];
     red[warp][lane] = s;
     __syncthreads();
@@ -599,33 +694,43 @@ void launch_norm_cast(const NormParams &p, int cast, int sms, cudaStream_t st) {
 
 template <bool BF16, bool RES>
 void launch_norm_v(const NormParams &p, int cast, int sms, cudaStream_t st) {
-    int v = p.vecs <= 128 ? 4 : p.vecs <= 1024 ? 2 : 4;
-    if (const char *e = std::getenv("NV")) v = std::atoi(e);
+    const int v = p.vecs <= 32 ? 1 : p.vecs <= 64 ? 2 : p.vecs <= 128 ? 4 : p.vecs <= 256 ? 1 : p.vecs <= (BF16 ? 512 : 1024) ? 2 : 4;
     if (v == 1) launch_norm_cast<BF16, RES, 1, 512>(p, cast, sms, st);
     else if (v == 2) launch_norm_cast<BF16, RES, 2, 512>(p, cast, sms, st);
     else if (p.vecs <= 4 * 512) launch_norm_cast<BF16, RES, 4, 512>(p, cast, sms, st);
     else launch_norm_cast<BF16, RES, 4, 1024>(p, cast, sms, st);
 }
 
+constexpr int BACK_SMEM = 226 * 1024;        // with the sums' 256 bytes, what a CTA can have
+constexpr int BACK_HALF = 112 * 1024;        // two CTAs to an SM
+
 template <bool BF16, bool RES, int V>
-cudaError_t launch_staged(BackParams &p, cudaStream_t st) {
+cudaError_t launch_staged(const BackParams &p, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     auto kern = norm_backward_kernel<BF16, RES, V, true>;
-    const int threads = threads_for(p.vecs, V), row = threads * V * (BF16 ? 16 : 32) * (RES ? 3 : 2);
-    p.stages = std::max(2, std::min(4, STAGE_BYTES / row));
-    const cudaError_t e = ensure_smem_limit(kern, 2 * 512 * 2 * 32 * 3, done);   // two rows of the widest
+    const cudaError_t e = ensure_smem_limit(kern, BACK_SMEM, done);
     if (e != cudaSuccess) return e;
-    kern<<<p.parts, threads, p.stages * row, st>>>(p);
+    kern<<<p.parts, p.threads * p.groups, p.groups * p.stages * (RES ? 3 : 2) * V * p.threads * 16, st>>>(p);
     return cudaGetLastError();
 }
 
 template <bool BF16, bool RES>
 cudaError_t launch_backward_v(BackParams &p, cudaStream_t st) {
-    int v = p.vecs <= 512 ? 1 : p.vecs <= 1024 ? 2 : 4;
-    if (const char *e = std::getenv("NB")) v = std::atoi(e);
-    if (v == 1) return launch_staged<BF16, RES, 1>(p, st);
-    if (v == 2) return launch_staged<BF16, RES, 2>(p, st);
-    norm_backward_kernel<BF16, RES, 4, false><<<p.parts, threads_for(p.vecs, 4), 0, st>>>(p);
+    const int v = p.pieces <= 64 ? 1 : p.pieces <= 512 ? 2 : 4;
+    p.threads = threads_for(p.pieces, v);
+    p.groups = std::max(1u, 256 / p.threads);
+    const int row = p.groups * (RES ? 3 : 2) * v * p.threads * 16;       // bytes of a stage
+    if (p.threads <= 512 && 2 * row <= BACK_SMEM) {
+        p.stages = std::max(2, std::min(4, BACK_HALF / row));
+        p.parts = static_cast<uint32_t>(std::min<int64_t>((p.rows + p.groups - 1) / p.groups, p.parts));
+        if (v == 1) return launch_staged<BF16, RES, 1>(p, st);
+        if (v == 2) return launch_staged<BF16, RES, 2>(p, st);
+        return launch_staged<BF16, RES, 4>(p, st);
+    }
+    p.groups = 1;
+    p.stages = 0;
+    p.threads = threads_for(p.pieces, 8);                                // cols <= 32768: at most 1024 (fp32)
+    norm_backward_kernel<BF16, RES, 8, false><<<p.parts, p.threads, 0, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -653,6 +758,8 @@ cudaError_t mx_launch_rmsnorm(const MxNormArgs &a, cudaStream_t st) {
                      : a.fmt == MX_E5M2 ? TO_E5M2
                      : a.fmt == MX_E2M1 ? TO_E2M1
                                         : TO_OTHERS;
+    auto on32 = [](const void *q, int64_t ld) { return !q || ((reinterpret_cast<uintptr_t>(q) | static_cast<uintptr_t>(ld * 4)) & 31u) == 0; };
+    p.wide = on32(a.x, a.ldx) && on32(a.residual, a.ldr) && on32(a.h, a.ldh) && on32(a.y, a.ldy);
     p.word_scales = (reinterpret_cast<uintptr_t>(a.scales) & 3u) == 0 && (a.sl != MX_SCALES_PLAIN || p.k_blocks % 4 == 0);
     if (a.xdt == MX_BF16) {
         if (p.res) launch_norm_v<true, true>(p, cast, a.num_sms, st);
@@ -670,15 +777,23 @@ cudaError_t mx_launch_rmsnorm_backward(const MxNormBackArgs &a, cudaStream_t st)
     p.dy = a.dy; p.h = a.h; p.dres = a.dres; p.rows = a.rows;
     p.lddy = a.lddy; p.ldh = a.ldh; p.lddres = a.lddres; p.lddx = a.lddx;
     p.cols = static_cast<uint32_t>(a.cols);
-    p.vecs = p.cols / 8;
+    p.pieces = p.cols / (a.xdt == MX_BF16 ? 8 : 4);
     p.w = a.weight; p.w_f32 = a.wdt == MX_F32; p.rstd = a.rstd;
     p.dx = a.dx; p.dw = a.dweight; p.part = a.part; p.parts = static_cast<uint32_t>(a.parts);
     p.inv_cols = 1.0f / static_cast<float>(a.cols);
     const cudaError_t e = a.xdt == MX_BF16 ? (p.dres ? launch_backward_v<true, true>(p, st) : launch_backward_v<true, false>(p, st))
                                            : (p.dres ? launch_backward_v<false, true>(p, st) : launch_backward_v<false, false>(p, st));
     if (e != cudaSuccess) return e;
-    norm_dweight_kernel<<<p.cols / 32, 32 * DW_WARPS, 0, st>>>(p.part, p.parts, p.cols, p.dw);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.cols / 32);
+    cfg.blockDim = dim3(32 * DW_WARPS);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_dweight_kernel, static_cast<const float *>(p.part), p.parts, p.cols, p.dw);
 }
 
 int mx_read_norm_bounds_status() {

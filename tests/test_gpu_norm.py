@@ -5,20 +5,20 @@ Forward tolerances.  h is one fp32 addition and one rounding, so it equals the
 same steps in numpy bit for bit.  rstd: the sum of squares is non-negative, so
 its relative error is at most d * 2^-24 for sums of depth d; a thread adds at
 most 32 squares (a multiply-add each), the tree over a CTA adds at most 10
-levels: d <= 42.  Division, addition of eps and the square root's and the
-last division's roundings add (42 + 1 + 1) / 2 + 2 = 24 half steps:
-|rstd - exact| <= 24 * 2^-24 * exact (a first-order bound; 25 covers the
-higher orders).  Given the kernel's rstd, y is two fp32 products and a
+levels: d <= 42.  The product with 1 / cols (itself rounded), the addition of
+eps and the rounded inverse square root make (42 + 2 + 1) / 2 + 1 < 24 half
+steps: |rstd - exact| <= 24 * 2^-24 * exact (a first-order bound; 25 covers
+the higher orders).  Given the kernel's rstd, y is two fp32 products and a
 rounding, and the codes and scales are the oracle's cast of the fp32 y: all
 equal bit for bit.
 
 Backward tolerances, with u = 2^-24, n = h * rstd, a = dy * w and c = mean(a n):
 n and a carry one rounding each, their product's sum at most 32 + 10 more and
-the division one, so c is off by at most 46 u mean|a n|.  dx = rstd (a - n c) +
+the product with 1 / cols two, so c is off by at most 46 u mean|a n|.  dx = rstd (a - n c) +
 dres: off by at most |rstd| (2 u |a| + 3 u |n c| + 46 u |n| mean|a n|) + 2 u
 |dx - dres| + u |dx|, and half a step of the output type.  dweight: n rounds
-once, a CTA adds its ceil(rows / 592) rows in turn and the parts are added in
-any order of at most 592: (ceil(rows / 592) + 594) u sum|dy n|.
+once, at most ceil(rows / 296) rows are added in turn, then at most 8 groups and
+296 parts in any order: (ceil(rows / 296) + 306) u sum|dy n|.
 """
 import numpy as np
 import pytest
@@ -272,7 +272,7 @@ def test_backward(rows, cols, dtype, res):
     assert np.all(err <= bound), (err / bound).max()
     want_w, abs_w = (g6 * n).sum(0), np.abs(g6 * n).sum(0)
     err = np.abs(host(dw).astype(np.float64) - want_w)
-    assert np.all(err <= 1.001 * (-(-rows // 592) + 594) * U * abs_w + 1e-38)
+    assert np.all(err <= 1.001 * (-(-rows // 296) + 306) * U * abs_w + 1e-38)
     # the same call again: the same bits
     dx2, dw2 = mx.rmsnorm_backward(dy, h, w, rstd, dres=dres)
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
