@@ -308,62 +308,71 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
     // A tile is the rows 4 w + {0..3} + {0, 32, 64, 96} of a scale atom, a 64-byte
     // run of each of its 512-byte groups.  Place g of a slot holds row
     // g % 4 + 64 (g / 4), place g + 8 the row 32 behind it: the rows of lane
-    // (g, t) in the products, and those whose 16-byte pieces t and t + 4 it
-    // copies.  A row past the last reads the last one again; its results are
-    // not stored.
-    const uint32_t cdst = ring32 + g * PITCH + t * 16;
+    // (g, t) in the products.  Lane 8 r + c copies the 16-byte piece c of rows r,
+    // r + 64, r + 32 and r + 96 (places r, r + 4, r + 8, r + 12): a row's 128
+    // bytes by eight lanes.  A row past the last reads the last one again; its
+    // results are not stored.
+    const uint32_t piece = lane & 7u, r0 = lane >> 3;
+    const uint32_t cdst = ring32 + r0 * PITCH + piece * 16;
     // lane l copies scale word l % 16 (of rows r + 32 q: 4 r + q) of group l / 16
     const uint32_t word = lane & 15u, sgroup = lane >> 4;
     const uint32_t sstep = p.sl == SL_PLAIN ? 4u : (p.sl == SL_MMA ? 512u : 2048u);     // bytes between groups
     const uint32_t sdst = ring32 + 16 * PITCH + lane * 4;
-    const uint8_t *src_lo, *src_hi, *src_s;                    // this lane's pieces of the next slice
+    const uint8_t *src, *src_s;                                // this lane's pieces of the next slice: row r's,
+    uint32_t off64, off32, off96;                              // and the others from there (K <= 2^24)
     auto set_tile = [&](uint32_t tile) {
-        const uint32_t row0 = tile / 8 * ATOM, w = tile % 8, row = row0 + 4 * w + (g & 3u) + 64 * (g >> 2);
-        const int64_t at = static_cast<int64_t>(part) * (SLICE / 2) + t * 16;
-        src_lo = p.codes + static_cast<int64_t>(min(row, p.n - 1)) * row_bytes + at;
-        src_hi = p.codes + static_cast<int64_t>(min(row + 32, p.n - 1)) * row_bytes + at;
+        const uint32_t row0 = tile / 8 * ATOM, w = tile % 8, row = min(row0 + 4 * w + r0, p.n - 1);
+        src = p.codes + static_cast<int64_t>(row) * row_bytes + static_cast<int64_t>(part) * (SLICE / 2) + piece * 16;
+        off64 = (min(row0 + 4 * w + r0 + 64, p.n - 1) - row) * row_bytes;
+        off32 = (min(row0 + 4 * w + r0 + 32, p.n - 1) - row) * row_bytes;
+        off96 = (min(row0 + 4 * w + r0 + 96, p.n - 1) - row) * row_bytes;
         const uint32_t srow = min(row0 + 4 * w + (word >> 2) + 32 * (word & 3u), p.n - 1);
         src_s = p.scales + (part * S::GROUPS + sgroup) * static_cast<uint64_t>(sstep) +
                 (p.sl == SL_PLAIN ? static_cast<uint64_t>(srow) * p.k_blocks
                                   : static_cast<uint64_t>(tile / 8) * p.k_groups * sstep + 64 * w + 4 * word);
     };
     const uint32_t code_step = p.parts * (SLICE / 2), scale_step = p.parts * S::GROUPS * sstep;
+    auto advance = [&] {
+        src += code_step;
+        src_s += scale_step;
+    };
+    auto issue_whole = [&](uint32_t slot) {                    // a slice of whole 16-byte pieces and scale words
+        copy_async<16>(cdst + slot, src);
+        copy_async<16>(cdst + slot + 4 * PITCH, src + off64);
+        copy_async<16>(cdst + slot + 8 * PITCH, src + off32);
+        copy_async<16>(cdst + slot + 12 * PITCH, src + off96);
+#pragma unroll
+        for (int i = 0; i < S::GROUPS / 2; ++i) copy_async<4>(sdst + slot + i * 128, src_s + 2 * i * sstep);
+        advance();
+    };
     auto issue = [&](uint32_t s, uint32_t slot) {
-        if (s < p.full) {                                      // (uniform) a whole slice of 16-byte pieces and words
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                copy_async<16>(cdst + slot + i * 64, src_lo + i * 64);
-                copy_async<16>(cdst + slot + 8 * PITCH + i * 64, src_hi + i * 64);
-            }
-#pragma unroll
-            for (int i = 0; i < S::GROUPS / 2; ++i) copy_async<4>(sdst + slot + i * 128, src_s + 2 * i * sstep);
-        } else {
-            // the end of K, rows of an odd number of 8-byte blocks, or scale rows off the words
+        if (s < p.full) {
+            issue_whole(slot);
+            return;
+        }
+        // the end of K, rows of an odd number of 8-byte blocks, or scale rows off the words
+        const uint32_t b = s * (SLICE / 2) + piece * 16, left = b < row_bytes ? row_bytes - b : 0u;
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t b = s * (SLICE / 2) + t * 16 + (i >> 1) * 64, left = b < row_bytes ? row_bytes - b : 0u;
-                const uint32_t dst = cdst + slot + (i & 1) * (8 * PITCH) + (i >> 1) * 64;
-                const uint8_t *from = (i & 1 ? src_hi : src_lo) + (i >> 1) * 64;
-                copy_async_part<8>(dst, left ? from : p.codes, left ? 8u : 0u);
-                copy_async_part<8>(dst + 8, left > 8 ? from + 8 : p.codes, left > 8 ? 8u : 0u);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t dst = cdst + slot + i * (4 * PITCH);
+            const uint8_t *from = src + (i == 0 ? 0u : i == 1 ? off64 : i == 2 ? off32 : off96);
+            copy_async_part<8>(dst, left ? from : p.codes, left ? 8u : 0u);
+            copy_async_part<8>(dst + 8, left > 8 ? from + 8 : p.codes, left > 8 ? 8u : 0u);
+        }
 #pragma unroll 1
-            for (int i = 0; i < S::GROUPS / 2; ++i) {
-                const uint32_t kg = s * S::GROUPS + sgroup + 2 * i;
-                const uint32_t n = kg * 4 < p.k_blocks ? min(p.k_blocks - kg * 4, 4u) : 0u;   // scales of this word
-                const uint8_t *from = n ? src_s + 2 * i * sstep : p.scales;
-                if (p.words) {
-                    copy_async_part<4>(sdst + slot + i * 128, from, n);
-                } else {
-                    uint32_t w = 0;
-                    for (uint32_t j = 0; j < n; ++j) w |= static_cast<uint32_t>(__ldg(from + j)) << (8 * j);
-                    *reinterpret_cast<uint32_t *>(ring + slot + 16 * PITCH + lane * 4 + i * 128) = w;
-                }
+        for (int i = 0; i < S::GROUPS / 2; ++i) {
+            const uint32_t kg = s * S::GROUPS + sgroup + 2 * i;
+            const uint32_t n = kg * 4 < p.k_blocks ? min(p.k_blocks - kg * 4, 4u) : 0u;   // scales of this word
+            const uint8_t *from = n ? src_s + 2 * i * sstep : p.scales;
+            if (p.words) {
+                copy_async_part<4>(sdst + slot + i * 128, from, n);
+            } else {
+                uint32_t w = 0;
+                for (uint32_t j = 0; j < n; ++j) w |= static_cast<uint32_t>(__ldg(from + j)) << (8 * j);
+                *reinterpret_cast<uint32_t *>(ring + slot + 16 * PITCH + lane * 4 + i * 128) = w;
             }
         }
-        src_lo += code_step;
-        src_hi += code_step;
-        src_s += scale_step;
+        advance();
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
@@ -441,6 +450,9 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
         issue(part, 0);
     }
     commit();
+    const uint8_t *codes_mine = ring + g * PITCH + 4 * t;
+    const uint32_t scale_mine = ring32 + 16 * PITCH + (g & 3u) * 16 + (g >> 2) * 8;
+    const bool act16[NT] = {};              // no token in bf16
     bool mixed = false;                     // a token of the window is in bf16 somewhere
     for (uint32_t pass = 0; pass < p.passes; ++pass) {
         const uint32_t stop = tile < tile_hi ? mine : 0u;
@@ -450,12 +462,26 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
                 if (w0 + pass > 0) __syncthreads();            // the last window has been read
                 mixed = __syncthreads_or(stage(w0));
             }
-            uint32_t s = w0 * p.parts + part, act_at = here * (SLICE * 2);
-            const uint8_t *fl = flags + here * (8 * NT);
             const uint32_t w1 = min(w0 + p.window, stop);
-            for (uint32_t i = w0; i < w1; ++i) {
+            const uint8_t *act[NT], *fl = flags + here * (8 * NT);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) act[j] = act_mine[j] + here * (SLICE * 2);
+            uint32_t s = w0 * p.parts + part, i = w0;
+            // steps whose next slice is whole, with every token in fp16: nothing to decide
+            for (; !XF32 && !mixed && i < w1 && i + 1 < stop && s + p.parts < p.full; ++i) {
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
                 __syncwarp();               // slice s is in, the other slot free
+                issue_whole(S::SLOT - slot);
+                commit();
+                slice_products<XF32, NV, NT, !XF32>(codes_mine + slot, scale_mine + slot, act, plane, lane, act16, acc);
+                slot = S::SLOT - slot;
+                s += p.parts;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) act[j] += p.share * (SLICE * 2);
+            }
+            for (; i < w1; ++i) {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                __syncwarp();
                 s += p.parts;
                 if (i + 1 < stop) {
                     issue(s, S::SLOT - slot);
@@ -464,11 +490,6 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
                     issue(part, S::SLOT - slot);
                 }
                 commit();
-                const uint8_t *codes = ring + slot + g * PITCH + 4 * t;
-                const uint32_t scale = ring32 + slot + 16 * PITCH + (g & 3u) * 16 + (g >> 2) * 8;
-                const uint8_t *act[NT];
-#pragma unroll
-                for (int j = 0; j < NT; ++j) act[j] = act_mine[j] + act_at;
                 bool bf16[NT], slow = XF32;
                 if (mixed) {
                     uint64_t any = 0;
@@ -479,10 +500,11 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
                     }
                     slow = __any_sync(0xffffffffu, any != 0);
                 }
-                if (XF32 || slow) slice_products<XF32, NV, NT, false>(codes, scale, act, plane, lane, bf16, acc);
-                else slice_products<XF32, NV, NT, !XF32>(codes, scale, act, plane, lane, bf16, acc);
+                if (XF32 || slow) slice_products<XF32, NV, NT, false>(codes_mine + slot, scale_mine + slot, act, plane, lane, bf16, acc);
+                else slice_products<XF32, NV, NT, !XF32>(codes_mine + slot, scale_mine + slot, act, plane, lane, act16, acc);
                 slot = S::SLOT - slot;
-                act_at += p.share * (SLICE * 2);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) act[j] += p.share * (SLICE * 2);
             }
         }
         if (p.parts == 1 && stop) {
