@@ -10,7 +10,6 @@ documented in include/mx.h.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -428,9 +427,21 @@ def _weight(device: int, t: torch.Tensor, cols: int):
     return t.data_ptr(), dt
 
 
-def _allocating(stream):
-    """New tensors belong to the stream that the call runs on."""
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """A new tensor on like's device, which belongs to the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _scale_bytes(layout: int, outer: int, blocks: int) -> int:
+    """mx_scales_bytes of `blocks` scales per row, without a call into the library."""
+    if layout == 0:
+        return outer * blocks
+    if layout not in (1, 2):
+        return 0                        # refused by the call
+    return -(-outer // 128) * 128 * (-(-blocks // 4) * 4) * (4 if layout == 2 else 1)
 
 
 def _handle(stream, device: int) -> int:
@@ -447,15 +458,12 @@ def _norm_args(x, weight, residual, h, y, want_y, rstd, want_rstd, stream):
     dev, xdt, shape, ldx = _first(x, "x")
     rows, cols = shape
     w, wdt = _weight(dev, weight, cols)
-    new_h, new_y, new_rstd = residual is not None and h is None, want_y and y is None, want_rstd and rstd is None
-    if new_h or new_y or new_rstd:
-        with _allocating(stream):
-            if new_h:
-                h = torch.empty(shape, dtype=x.dtype, device=x.device)
-            if new_y:
-                y = torch.empty(shape, dtype=x.dtype, device=x.device)
-            if new_rstd:
-                rstd = torch.empty((rows,), dtype=torch.float32, device=x.device)
+    if residual is not None and h is None:
+        h = _empty(shape, x.dtype, x, stream)
+    if want_y and y is None:
+        y = _empty(shape, x.dtype, x, stream)
+    if want_rstd and rstd is None:
+        rstd = _empty((rows,), torch.float32, x, stream)
     r = hp = yp = rp = None
     ldr = ldh = ldy = 0
     if residual is not None:
@@ -503,14 +511,13 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
     f, sl = _fmt(fmt), _layout(scale_layout)
     L = _lib or lib()
     rows, cols = ins[2], ins[3]
-    n_codes, n_scales = L.mx_codes_bytes(f, rows, cols), L.mx_scales_bytes(sl, rows, cols)
-    if codes is None or scales is None:
-        with _allocating(stream):
-            if codes is None:
-                codes = torch.empty((rows, codes_row_bytes(f, cols)), dtype=torch.uint8, device=x.device)
-            if scales is None:
-                scales = torch.empty(max(n_scales, 1), dtype=torch.uint8, device=x.device)
-    c = _flat(dev, codes, "codes", n_codes, torch.uint8)
+    row_bytes = cols * FMT_BITS.get(f, 0) // 8
+    n_scales = _scale_bytes(sl, rows, -(-cols // 32))
+    if codes is None:
+        codes = _empty((rows, row_bytes), torch.uint8, x, stream)
+    if scales is None:
+        scales = _empty(max(n_scales, 1), torch.uint8, x, stream)
+    c = _flat(dev, codes, "codes", rows * row_bytes, torch.uint8)
     s = _flat(dev, scales, "scales", n_scales, torch.uint8)
     rc = L.mx_rmsnorm_quantize(*ins, eps, f, ROUND[rnd] if isinstance(rnd, str) else int(rnd), seed & (2**64 - 1),
                                *outs, c, s, sl, _handle(stream, dev))
@@ -535,14 +542,12 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rs
     dx, dweight = out if out is not None else (None, None)
     L = _lib or lib()
     n_ws = L.mx_rmsnorm_backward_workspace_bytes(rows, cols)
-    if dx is None or dweight is None or workspace is None:
-        with _allocating(stream):
-            if dx is None:
-                dx = torch.empty(shape, dtype=dy.dtype, device=dy.device)
-            if dweight is None:
-                dweight = torch.empty((cols,), dtype=torch.float32, device=dy.device)
-            if workspace is None:
-                workspace = torch.empty(max(n_ws, 1), dtype=torch.uint8, device=dy.device)
+    if dx is None:
+        dx = _empty(shape, dy.dtype, dy, stream)
+    if dweight is None:
+        dweight = _empty((cols,), torch.float32, dy, stream)
+    if workspace is None:
+        workspace = _empty(max(n_ws, 1), torch.uint8, dy, stream)
     ldh = _matrix(dev, h, "h", shape, dy.dtype)
     lddx = _matrix(dev, dx, "dx", shape, dy.dtype)
     lddres = _matrix(dev, dres, "dres", shape, dy.dtype) if dres is not None else 0
@@ -570,8 +575,7 @@ def _gemv_args(x, N, K, out_dtype, out, stream):
         raise ValueError("x must have K columns")
     M = shape[0]
     if out is None:
-        with _allocating(stream):
-            out = torch.empty((M, N), dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+        out = _empty((M, N), x.dtype if out_dtype is None else out_dtype, x, stream)
     ydt = DTYPE.get(out.dtype)
     if ydt is None:
         raise TypeError("the output must be float32 or bfloat16")
@@ -589,8 +593,8 @@ def gemv(w_codes: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, N: int,
     f, sl = _fmt(fmt), _layout(scale_layout)
     dev, out, ins, outs = _gemv_args(x, N, K, out_dtype, out, stream)
     L = _lib or lib()
-    c = _flat(dev, w_codes, "w_codes", L.mx_codes_bytes(f, N, K), torch.uint8)
-    s = _flat(dev, w_scales, "w_scales", L.mx_scales_bytes(sl, N, K), torch.uint8)
+    c = _flat(dev, w_codes, "w_codes", N * K // 2, torch.uint8)
+    s = _flat(dev, w_scales, "w_scales", _scale_bytes(sl, N, -(-K // 32)), torch.uint8)
     rc = L.mx_gemv(c, s, f, sl, *ins, alpha, *outs, _handle(stream, dev))
     if rc != MX_OK:
         raise MxError(rc, "mx_gemv")
@@ -607,8 +611,9 @@ def gemv_nvfp4(w, x: torch.Tensor, N: int, K: int, domain_rows: int = 0, alpha: 
     dev, out, ins, outs = _gemv_args(x, N, K, out_dtype, out, stream)
     L = _lib or lib()
     c = _flat(dev, codes, "codes", N * K // 2, torch.uint8)
-    s = _flat(dev, scales, "scales", L.mx_nvfp4_scales_bytes(sl, N, K), torch.uint8)
-    e = _flat(dev, enc, "enc_scales", L.mx_nvfp4_domains(N, domain_rows), torch.float32)
+    s = _flat(dev, scales, "scales", _scale_bytes(sl, N, -(-K // 16)), torch.uint8)
+    domains = -(-N // domain_rows) if domain_rows > 0 else 1         # a negative one is refused by the call
+    e = _flat(dev, enc, "enc_scales", domains, torch.float32)
     rc = L.mx_gemv_nvfp4(c, s, e, domain_rows, sl, *ins, alpha, *outs, _handle(stream, dev))
     if rc != MX_OK:
         raise MxError(rc, "mx_gemv_nvfp4")
