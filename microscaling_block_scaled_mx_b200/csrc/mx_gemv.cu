@@ -298,6 +298,10 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
     uint8_t *flags = acts + S::PLANES * plane;                 // [win][8 NT]: the token is in bf16
     const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
 
+    // launched while the stream's last kernel may still run (see the launch): no
+    // global memory is touched before it has ended and its writes are visible
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t t0 = blockIdx.y * (8 * NT), count = min(p.tokens - t0, 8u * NT);
     const uint32_t size = 1u << p.size_log, rank = blockIdx.x & (size - 1), cluster = blockIdx.x >> p.size_log;
     const uint32_t tile_lo = cluster * p.each + min(cluster, p.extra);
@@ -639,12 +643,17 @@ cudaError_t launch(GemvParams &p, int sms, cudaStream_t st) {
     cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = S::smem(warps, p.tile, p.window * p.share);
     cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = size;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = size > 1 ? 1 : 0;
+    // Programmatic serialization: this kernel's CTAs may start before the stream's
+    // last kernel has drained.  Back to back, one token x 28672 x 4096 takes 15.9 us
+    // a call instead of 18.4, eight x 4096 x 14336 15.1 instead of 16.6.
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = size;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = size > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kern, p);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }

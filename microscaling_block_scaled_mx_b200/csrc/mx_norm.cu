@@ -41,6 +41,15 @@ struct NormParams {
     uint64_t codes_cap, scales_cap;
 };
 
+// The kernels of this unit may be launched while the stream's last kernel still
+// runs (programmatic serialization, which saves 1 to 3 us between short ones);
+// they touch no global memory before it has ended and its writes are visible,
+// and let their own successor be launched in the same way.
+__device__ __forceinline__ void after_predecessor() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Two fp32 values in a register pair, and IEEE operations on both at a time.
 using f2 = uint64_t;
 __device__ __forceinline__ f2 pair(float lo, float hi) {
@@ -314,6 +323,7 @@ __global__ void __launch_bounds__(T, 1) norm_kernel(const __grid_constant__ Norm
     constexpr bool AHEAD = V * (BF16 ? 1 : 2) <= 4 && T <= 512;
     constexpr bool WIDE = V <= 2;                              // h stays widened between its two uses
     constexpr int SIZE = BF16 ? 2 : 4;
+    after_predecessor();
     __shared__ __align__(16) float red[2][32];
     Raw<BF16> x[AHEAD ? V : 1], r[AHEAD && RES ? V : 1];
     f2 w[AHEAD ? V : 1][4];
@@ -502,6 +512,7 @@ template <bool BF16, bool RES, int V, bool STAGED>
 __global__ void __launch_bounds__(STAGED || BF16 ? 512 : 1024, 1) norm_backward_kernel(const __grid_constant__ BackParams p) {
     using P = Piece<BF16>;
     constexpr int ARRAYS = RES ? 3 : 2;
+    after_predecessor();
     __shared__ __align__(16) float red[2][32];
     extern __shared__ __align__(16) uint4 ring[];              // [group][stage][array][piece]
     const uint32_t n = p.threads, group = threadIdx.x / n, t = threadIdx.x - group * n;
@@ -540,7 +551,6 @@ __global__ void __launch_bounds__(STAGED || BF16 ? 512 : 1024, 1) norm_backward_
         for (int j = 0; j < P::PAIRS; ++j) acc[i][j] = 0;
         if (STAGED && i * n + t < p.pieces) P::weights(p.w, p.w_f32, (i * n + t) * P::VALUES, w[STAGED ? i : 0]);
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");      // the sum of the parts may be launched
     clear_sums(red);
     float rstd = first < p.rows ? p.rstd[first] : 0.0f;
     int turn = 0;
@@ -644,13 +654,12 @@ __global__ void __launch_bounds__(STAGED || BF16 ? 512 : 1024, 1) norm_backward_
 }
 
 // dweight[c] = the sum of the parts: 32 columns to a CTA, warp w adds parts w,
-// w + 32, ..., and the warps' sums are added in their order.  Launched while the
-// backward kernel still runs; it waits for that kernel's end before it reads.
+// w + 32, ..., and the warps' sums are added in their order.
 constexpr int DW_WARPS = 32;
 __global__ void __launch_bounds__(32 * DW_WARPS) norm_dweight_kernel(const float *part, uint32_t parts, uint32_t cols, float *dw) {
     __shared__ float red[DW_WARPS][32];
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;    // cols % 32 == 0
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_predecessor();
     float s = 0.0f;
 #pragma unroll 10
     for (uint32_t i = warp; i < parts; i += DW_WARPS) s += part[static_cast<int64_t>(i) * cols + c];
@@ -660,6 +669,22 @@ __global__ void __launch_bounds__(32 * DW_WARPS) norm_dweight_kernel(const float
 #pragma unroll
     for (int i = 1; i < DW_WARPS; ++i) s += red[i][lane];
     dw[c] = s;
+}
+
+// Launches a kernel that begins with after_predecessor().
+template <typename Kern, typename... Args>
+cudaError_t launch_early(Kern kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t st, const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 int threads_for(uint32_t vecs, int v) { return static_cast<int>((vecs + v - 1) / v + 31) / 32 * 32; }
@@ -673,15 +698,15 @@ int64_t resident(Kern kern, int threads, int sms) {
 }
 
 template <bool BF16, bool RES, int V, int T, int CAST>
-void launch_norm(const NormParams &p, int sms, cudaStream_t st) {
+cudaError_t launch_norm(const NormParams &p, int sms, cudaStream_t st) {
     auto kern = norm_kernel<BF16, RES, V, T, CAST>;
     const int threads = threads_for(p.vecs, V);
     const int64_t most = p.rows <= sms ? p.rows : resident(kern, threads, sms);
-    kern<<<static_cast<unsigned>(p.rows < most ? p.rows : most), threads, 0, st>>>(p);
+    return launch_early(kern, static_cast<unsigned>(p.rows < most ? p.rows : most), threads, 0, st, p);
 }
 
 template <bool BF16, bool RES, int V, int T>
-void launch_norm_cast(const NormParams &p, int cast, int sms, cudaStream_t st) {
+cudaError_t launch_norm_cast(const NormParams &p, int cast, int sms, cudaStream_t st) {
     switch (cast) {
         case NO_CAST: return launch_norm<BF16, RES, V, T, NO_CAST>(p, sms, st);
         case TO_E4M3: return launch_norm<BF16, RES, V, T, TO_E4M3>(p, sms, st);
@@ -693,12 +718,12 @@ void launch_norm_cast(const NormParams &p, int cast, int sms, cudaStream_t st) {
 }
 
 template <bool BF16, bool RES>
-void launch_norm_v(const NormParams &p, int cast, int sms, cudaStream_t st) {
+cudaError_t launch_norm_v(const NormParams &p, int cast, int sms, cudaStream_t st) {
     const int v = p.vecs <= 32 ? 1 : p.vecs <= 64 ? 2 : p.vecs <= 128 ? 4 : p.vecs <= 256 ? 1 : p.vecs <= (BF16 ? 512 : 1024) ? 2 : 4;
-    if (v == 1) launch_norm_cast<BF16, RES, 1, 512>(p, cast, sms, st);
-    else if (v == 2) launch_norm_cast<BF16, RES, 2, 512>(p, cast, sms, st);
-    else if (p.vecs <= 4 * 512) launch_norm_cast<BF16, RES, 4, 512>(p, cast, sms, st);
-    else launch_norm_cast<BF16, RES, 4, 1024>(p, cast, sms, st);
+    if (v == 1) return launch_norm_cast<BF16, RES, 1, 512>(p, cast, sms, st);
+    if (v == 2) return launch_norm_cast<BF16, RES, 2, 512>(p, cast, sms, st);
+    if (p.vecs <= 4 * 512) return launch_norm_cast<BF16, RES, 4, 512>(p, cast, sms, st);
+    return launch_norm_cast<BF16, RES, 4, 1024>(p, cast, sms, st);
 }
 
 constexpr int BACK_SMEM = 226 * 1024;        // with the sums' 256 bytes, what a CTA can have
@@ -710,8 +735,7 @@ cudaError_t launch_staged(const BackParams &p, cudaStream_t st) {
     auto kern = norm_backward_kernel<BF16, RES, V, true>;
     const cudaError_t e = ensure_smem_limit(kern, BACK_SMEM, done);
     if (e != cudaSuccess) return e;
-    kern<<<p.parts, p.threads * p.groups, p.groups * p.stages * (RES ? 3 : 2) * V * p.threads * 16, st>>>(p);
-    return cudaGetLastError();
+    return launch_early(kern, p.parts, p.threads * p.groups, p.groups * p.stages * (RES ? 3 : 2) * V * p.threads * 16, st, p);
 }
 
 template <bool BF16, bool RES>
@@ -730,8 +754,7 @@ cudaError_t launch_backward_v(BackParams &p, cudaStream_t st) {
     p.groups = 1;
     p.stages = 0;
     p.threads = threads_for(p.pieces, 8);                                // cols <= 32768: at most 1024 (fp32)
-    norm_backward_kernel<BF16, RES, 8, false><<<p.parts, p.threads, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_early(norm_backward_kernel<BF16, RES, 8, false>, p.parts, p.threads, 0, st, p);
 }
 
 }  // namespace mxnorm
@@ -761,14 +784,8 @@ cudaError_t mx_launch_rmsnorm(const MxNormArgs &a, cudaStream_t st) {
     auto on32 = [](const void *q, int64_t ld) { return !q || ((reinterpret_cast<uintptr_t>(q) | static_cast<uintptr_t>(ld * 4)) & 31u) == 0; };
     p.wide = on32(a.x, a.ldx) && on32(a.residual, a.ldr) && on32(a.h, a.ldh) && on32(a.y, a.ldy);
     p.word_scales = (reinterpret_cast<uintptr_t>(a.scales) & 3u) == 0 && (a.sl != MX_SCALES_PLAIN || p.k_blocks % 4 == 0);
-    if (a.xdt == MX_BF16) {
-        if (p.res) launch_norm_v<true, true>(p, cast, a.num_sms, st);
-        else launch_norm_v<true, false>(p, cast, a.num_sms, st);
-    } else {
-        if (p.res) launch_norm_v<false, true>(p, cast, a.num_sms, st);
-        else launch_norm_v<false, false>(p, cast, a.num_sms, st);
-    }
-    return cudaGetLastError();
+    if (a.xdt == MX_BF16) return p.res ? launch_norm_v<true, true>(p, cast, a.num_sms, st) : launch_norm_v<true, false>(p, cast, a.num_sms, st);
+    return p.res ? launch_norm_v<false, true>(p, cast, a.num_sms, st) : launch_norm_v<false, false>(p, cast, a.num_sms, st);
 }
 
 cudaError_t mx_launch_rmsnorm_backward(const MxNormBackArgs &a, cudaStream_t st) {
@@ -784,16 +801,8 @@ cudaError_t mx_launch_rmsnorm_backward(const MxNormBackArgs &a, cudaStream_t st)
     const cudaError_t e = a.xdt == MX_BF16 ? (p.dres ? launch_backward_v<true, true>(p, st) : launch_backward_v<true, false>(p, st))
                                            : (p.dres ? launch_backward_v<false, true>(p, st) : launch_backward_v<false, false>(p, st));
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.cols / 32);
-    cfg.blockDim = dim3(32 * DW_WARPS);
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_dweight_kernel, static_cast<const float *>(p.part), p.parts, p.cols, p.dw);
+    return launch_early(norm_dweight_kernel, p.cols / 32, 32 * DW_WARPS, 0, st, static_cast<const float *>(p.part), p.parts,
+                        p.cols, p.dw);
 }
 
 int mx_read_norm_bounds_status() {
