@@ -54,7 +54,6 @@ struct GemvParams {
     const float *enc;          // NVFP4 encode scales, one per `lines` weight rows
     int64_t lines;
     int sl;
-    bool words;                // every scale word is whole and aligned (plain scales may not be)
     uint32_t full;             // slices that are whole, in 16-byte pieces of codes and scale words
     const void *x;
     int64_t ldx;
@@ -285,7 +284,8 @@ __device__ __forceinline__ void store_y(const GemvParams &p, uint32_t tok, uint3
     else static_cast<__nv_bfloat16 *>(p.y)[off] = __float2bfloat16_rn(v);
 }
 
-template <bool XF32, bool NV, int NT>
+// BYTES: plain scales whose rows are not whole aligned words.
+template <bool XF32, bool NV, int NT, bool BYTES>
 __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_constant__ GemvParams p) {
     using S = Shape<XF32, NV, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -349,34 +349,53 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
         for (int i = 0; i < S::GROUPS / 2; ++i) copy_async<4>(sdst + slot + i * 128, src_s + 2 * i * sstep);
         advance();
     };
+    // Any slice.  BYTES: the scales are read byte by byte into registers, and
+    // place_scales puts them into the slot after the products of the slice before,
+    // when they have come.
+    constexpr int WORDS = S::GROUPS / 2;
+    uint32_t bytes[BYTES ? WORDS : 1][4];
     auto issue = [&](uint32_t s, uint32_t slot) {
         if (s < p.full) {
             issue_whole(slot);
             return;
         }
-        // the end of K, rows of an odd number of 8-byte blocks, or scale rows off the words
         const uint32_t b = s * (SLICE / 2) + piece * 16, left = b < row_bytes ? row_bytes - b : 0u;
-#pragma unroll 1
+        const bool whole = (s + 1) * (SLICE / 2) <= row_bytes;                 // (uniform)
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t dst = cdst + slot + i * (4 * PITCH);
             const uint8_t *from = src + (i == 0 ? 0u : i == 1 ? off64 : i == 2 ? off32 : off96);
-            copy_async_part<8>(dst, left ? from : p.codes, left ? 8u : 0u);
-            copy_async_part<8>(dst + 8, left > 8 ? from + 8 : p.codes, left > 8 ? 8u : 0u);
+            if (whole && (!NV || row_bytes % 16 == 0)) {
+                copy_async<16>(dst, from);
+            } else if (whole) {                                // rows of an odd number of 8-byte blocks
+                copy_async<8>(dst, from);
+                copy_async<8>(dst + 8, from + 8);
+            } else {
+                copy_async_part<8>(dst, left ? from : p.codes, left ? 8u : 0u);
+                copy_async_part<8>(dst + 8, left > 8 ? from + 8 : p.codes, left > 8 ? 8u : 0u);
+            }
         }
-#pragma unroll 1
-        for (int i = 0; i < S::GROUPS / 2; ++i) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
             const uint32_t kg = s * S::GROUPS + sgroup + 2 * i;
             const uint32_t n = kg * 4 < p.k_blocks ? min(p.k_blocks - kg * 4, 4u) : 0u;   // scales of this word
-            const uint8_t *from = n ? src_s + 2 * i * sstep : p.scales;
-            if (p.words) {
-                copy_async_part<4>(sdst + slot + i * 128, from, n);
+            const uint8_t *from = src_s + 2 * i * sstep;
+            if (!BYTES) {
+                copy_async_part<4>(sdst + slot + i * 128, n ? from : p.scales, n);
             } else {
-                uint32_t w = 0;
-                for (uint32_t j = 0; j < n; ++j) w |= static_cast<uint32_t>(__ldg(from + j)) << (8 * j);
-                *reinterpret_cast<uint32_t *>(ring + slot + 16 * PITCH + lane * 4 + i * 128) = w;
+#pragma unroll
+                for (uint32_t j = 0; j < 4; ++j) bytes[BYTES ? i : 0][j] = j < n ? __ldg(from + j) : 0u;
             }
         }
         advance();
+    };
+    auto place_scales = [&](uint32_t slot) {
+        if (!BYTES) return;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i)
+            *reinterpret_cast<uint32_t *>(ring + slot + 16 * PITCH + lane * 4 + i * 128) =
+                bytes[BYTES ? i : 0][0] | (bytes[BYTES ? i : 0][1] << 8) | (bytes[BYTES ? i : 0][2] << 16) |
+                (bytes[BYTES ? i : 0][3] << 24);
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
@@ -452,6 +471,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
     if (mine) {
         set_tile(tile);
         issue(part, 0);
+        place_scales(0);
     }
     commit();
     const uint8_t *codes_mine = ring + g * PITCH + 4 * t;
@@ -472,7 +492,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
             for (int j = 0; j < NT; ++j) act[j] = act_mine[j] + here * (SLICE * 2);
             uint32_t s = w0 * p.parts + part, i = w0;
             // steps whose next slice is whole, with every token in fp16: nothing to decide
-            for (; !XF32 && !mixed && i < w1 && i + 1 < stop && s + p.parts < p.full; ++i) {
+            for (; !XF32 && !mixed && i < w1 && i + 1 < stop && s + p.parts < p.full && !BYTES; ++i) {
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
                 __syncwarp();               // slice s is in, the other slot free
                 issue_whole(S::SLOT - slot);
@@ -487,11 +507,10 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
                 __syncwarp();
                 s += p.parts;
-                if (i + 1 < stop) {
-                    issue(s, S::SLOT - slot);
-                } else if (more) {
-                    set_tile(tile + p.lanes);
-                    issue(part, S::SLOT - slot);
+                const bool ahead = i + 1 < stop || more;
+                if (ahead) {
+                    if (i + 1 == stop) set_tile(tile + p.lanes);
+                    issue(i + 1 == stop ? part : s, S::SLOT - slot);
                 }
                 commit();
                 bool bf16[NT], slow = XF32;
@@ -507,6 +526,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
                 if (XF32 || slow) slice_products<XF32, NV, NT, false>(codes_mine + slot, scale_mine + slot, act, plane, lane, bf16, acc);
                 else slice_products<XF32, NV, NT, !XF32>(codes_mine + slot, scale_mine + slot, act, plane, lane, act16, acc);
                 slot = S::SLOT - slot;
+                if (ahead) place_scales(slot);
 #pragma unroll
                 for (int j = 0; j < NT; ++j) act[j] += p.share * (SLICE * 2);
             }
@@ -575,11 +595,11 @@ uint32_t max_clusters(Kern kern, int size, int sms) {
     return n;
 }
 
-template <bool XF32, bool NV, int NT>
-cudaError_t launch(GemvParams &p, int sms, cudaStream_t st) {
+template <bool XF32, bool NV, int NT, bool BYTES>
+cudaError_t launch_kernel(GemvParams &p, int sms, cudaStream_t st) {
     using S = Shape<XF32, NV, NT>;
     static std::atomic<uint64_t> done{0};
-    auto kern = gemv_kernel<XF32, NV, NT>;
+    auto kern = gemv_kernel<XF32, NV, NT, BYTES>;
     cudaError_t e = ensure_smem_limit(kern, SMEM_MAX, done);
     if (e != cudaSuccess) return e;
     p.tile = p.tokens < 8 * NT ? p.tokens : 8 * NT;
@@ -658,6 +678,11 @@ cudaError_t launch(GemvParams &p, int sms, cudaStream_t st) {
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
+template <bool XF32, bool NV, int NT>
+cudaError_t launch(GemvParams &p, bool bytes, int sms, cudaStream_t st) {
+    return bytes ? launch_kernel<XF32, NV, NT, true>(p, sms, st) : launch_kernel<XF32, NV, NT, false>(p, sms, st);
+}
+
 }  // namespace mxgemv
 
 cudaError_t mx_launch_gemv(const MxGemvArgs &a, cudaStream_t st) {
@@ -670,13 +695,13 @@ cudaError_t mx_launch_gemv(const MxGemvArgs &a, cudaStream_t st) {
     p.k_blocks = p.k / (a.enc ? 16 : 32);
     p.k_groups = (p.k_blocks + 3) / 4;
     p.slices = (p.k + SLICE - 1) / SLICE;
-    p.words = a.sl != SL_PLAIN || (p.k_blocks % 4 == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 3u) == 0);
-    p.full = p.words && p.k % 32 == 0 ? p.k / SLICE : 0;
+    const bool bytes = a.sl == SL_PLAIN && (p.k_blocks % 4 != 0 || (reinterpret_cast<uintptr_t>(a.scales) & 3u) != 0);
+    p.full = !bytes && p.k % 32 == 0 ? p.k / SLICE : 0;
     const uint32_t rest = p.n % ATOM;                              // rows of the last atom: a tile starts at each 4th of the first 32
     p.tiles = p.n / ATOM * 8 + (rest >= 32 ? 8 : (rest + 3) / 4);
     p.alpha = a.alpha; p.y = a.y; p.y_f32 = a.ydt == MX_F32; p.ldy = a.ldy;
     const bool nv = a.enc != nullptr;
-    if (a.xdt == MX_F32) return nv ? launch<true, true, 1>(p, a.num_sms, st) : launch<true, false, 1>(p, a.num_sms, st);
-    if (p.tokens <= 8) return nv ? launch<false, true, 1>(p, a.num_sms, st) : launch<false, false, 1>(p, a.num_sms, st);
-    return nv ? launch<false, true, 2>(p, a.num_sms, st) : launch<false, false, 2>(p, a.num_sms, st);
+    if (a.xdt == MX_F32) return nv ? launch<true, true, 1>(p, bytes, a.num_sms, st) : launch<true, false, 1>(p, bytes, a.num_sms, st);
+    if (p.tokens <= 8) return nv ? launch<false, true, 1>(p, bytes, a.num_sms, st) : launch<false, false, 1>(p, bytes, a.num_sms, st);
+    return nv ? launch<false, true, 2>(p, bytes, a.num_sms, st) : launch<false, false, 2>(p, bytes, a.num_sms, st);
 }

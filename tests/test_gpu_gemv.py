@@ -135,6 +135,111 @@ def test_tokens_are_independent():
             assert torch.equal(mx.gemv_nvfp4(ws, x[a:b], N, K, 32), whole_nv[a:b])
 
 
+@pytest.mark.parametrize("N,K", [(300, 8192), (4100, 4096), (40, 14336)])
+def test_a_batch_of_any_size_gives_the_same(N, K):
+    """The work is cut differently for one token and for sixteen, the sums are not;
+    and a token whose neighbours need bf16 products keeps its bits."""
+    codes, scales, _ = mx_weights(N, K, "mma", 40)
+    ws, _ = nv_weights(N, K, "mma_x4", 0, 41)
+    x = activations(24, K, torch.bfloat16, 42)
+    x[5, 3] = 5000.0                                # past what fp16 takes, in the first slice
+    x[17, K - 1] = 1e-12                            # below it, in the last
+    x[20] *= 2.0 ** -60
+    whole = mx.gemv(codes, scales, x, N, K), mx.gemv_nvfp4(ws, x, N, K, scale_layout="mma_x4")
+    for a, b in ((0, 1), (4, 5), (5, 6), (16, 18), (17, 18), (0, 8), (8, 24), (20, 21)):
+        assert torch.equal(mx.gemv(codes, scales, x[a:b], N, K), whole[0][a:b]), (a, b)
+        assert torch.equal(mx.gemv_nvfp4(ws, x[a:b], N, K, scale_layout="mma_x4"), whole[1][a:b]), (a, b)
+
+
+@pytest.mark.parametrize("M", [1, 9])
+def test_more_rows_than_one_pass(M):
+    N, K = 70001, 96
+    codes, scales, w = mx_weights(N, K, "mma", 43)
+    x = activations(M, K, torch.bfloat16, 44)
+    check(mx.gemv(codes, scales, x, N, K), x, w)
+    codes, scales, w = mx_weights(N, K, "plain", 45)
+    check(mx.gemv(codes, scales, x, N, K, scale_layout="plain"), x, w)
+
+
+def test_calls_back_to_back():
+    """A chain of calls, each reading what the one before wrote, with other work
+    between them, as the same calls one at a time."""
+    N = K = 2048
+    codes, scales, _ = mx_weights(N, K, "mma", 46, 114, 120)
+    ws, _ = nv_weights(N, K, "mma", 0, 47)
+    gamma = torch.ones(K, device=dev())
+    x = activations(2, K, torch.bfloat16, 48)
+
+    def chain(pause):
+        h, y = x.clone(), None
+        for k in range(12):
+            y, h, _ = mx.rmsnorm(h, gamma, residual=h if y is None else y)
+            pause()
+            y = mx.gemv(codes, scales, y, N, K) if k % 2 else mx.gemv_nvfp4(ws, y, N, K)
+            pause()
+            if k % 3 == 0:
+                y = y * 0.5
+                pause()
+        return h, y
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(20):
+        got = chain(lambda: None)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain(lambda: None)
+    for _ in range(5):
+        graph.replay()
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def test_two_streams_at_once():
+    """Calls on two streams at a time, weights shared."""
+    N, K = 4096, 2048
+    codes, scales, _ = mx_weights(N, K, "mma", 49)
+    xs = [activations(3, K, torch.bfloat16, 50 + i) for i in range(2)]
+    want = [mx.gemv(codes, scales, x, N, K) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(30):
+        for i, s in enumerate(streams):
+            got[i].append(mx.gemv(codes, scales, xs[i], N, K, stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) for y in got[i])
+
+
+FIRST_IN_A_GRAPH = """
+import sys, torch
+sys.path.insert(0, {root!r})
+from microscaling_block_scaled_mx_b200 import mx
+d = dict(device="cuda")
+codes = torch.full((256, 512), 0x22, dtype=torch.uint8, **d)
+scales = torch.full((mx.scales_bytes("mma", 256, 1024),), 127, dtype=torch.uint8, **d)
+x, w = torch.ones(2, 1024, **d).bfloat16(), torch.ones(1024, **d)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    y, h, rstd = mx.rmsnorm(x, w, 0.0, residual=x, with_rstd=True)
+    q = mx.rmsnorm_quantize(x, w)
+    out = mx.gemv(codes, scales, y, 256, 1024)
+    dx, dw = mx.rmsnorm_backward(y, h, w, rstd)
+graph.replay()
+torch.cuda.synchronize()
+assert (out == 1024).all() and (h == 2).all() and (dw == 2).all()
+"""
+
+
+def test_first_call_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_A_GRAPH.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 def test_layouts_agree():
     N, K = 300, 1184
     x = activations(3, K, torch.bfloat16, 10)
