@@ -428,10 +428,11 @@ MX_API int mx_gemm_quantize_x4(const void *a_codes, const void *a_scales, mx_fmt
  * producer that writes what its consumer reads, "Format-Aware Fusion for Fast
  * FP4 Pretraining", abstract).  Per row:
  *    h    = x + residual, rounded to xdt (with a residual; else h = x)
- *    rstd = 1 / sqrt(sum_c h_c^2 / cols + eps)
+ *    rstd = 1 / sqrt(sum_c h_c^2 * (1 / cols) + eps)
  *    y_c  = (h_c * rstd) * weight_c
  * The sum of squares is fp32 in an order fixed by cols and xdt; every other
- * step is one IEEE fp32 operation.  The squares overflow fp32 for |h| above
+ * step is one IEEE fp32 operation (the inverse square root and 1 / cols are
+ * each rounded once), so a row's result does not depend on the other rows.  The squares overflow fp32 for |h| above
  * 1.8e19: rstd is then 0.  A NaN in h makes its whole row of y NaN; an Inf
  * makes rstd 0, and y is NaN at the Inf and zero elsewhere.
  *
@@ -484,6 +485,10 @@ MX_API int mx_rmsnorm_backward(const void *dy, mx_dtype xdt, int64_t rows, int64
                                void *workspace, size_t ws_bytes, void *stream);
 MX_API size_t mx_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
 
+/* The five calls above and below may start before the stream's preceding kernel
+ * has drained (programmatic stream serialization); they read and write nothing
+ * before it has ended. */
+
 /*
  * mx_gemv, mx_gemv_nvfp4 -- y = alpha * x W^T for a few tokens (rows of x),
  * the weights in MXFP4 or NVFP4 and the activations as they are (section 4's
@@ -491,9 +496,10 @@ MX_API size_t mx_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
  * for each handful of tokens, and four bits of it).  The weights' buffers are
  * those of mx_gemm's and mx_gemm_nvfp4's B operand, so that one copy of the
  * weights serves both.  Products with the codes are exact, sums are fp32 in an
- * order fixed by N, K, the layout and the types, whatever the other tokens
- * are; the scales multiply fp32 partial sums (MXFP4) or enter exactly
- * (NVFP4: 2^8-scaled inside), and the result is rounded once to ydt.
+ * order fixed by N, K and the types, whatever the other tokens are and however
+ * many; the scales multiply fp32 partial sums (MXFP4) or the codes, exactly
+ * (NVFP4).  The sum is multiplied by alpha (NVFP4: fl32(alpha / E) of its row's
+ * domain) in fp32 and rounded to ydt.
  *
  *  w_codes  device, N x K codes (K / 2 bytes per row), 16-byte aligned.
  *  fw       MX_E2M1 (MX_ERR_UNSUPPORTED for the other formats).
@@ -504,12 +510,14 @@ MX_API size_t mx_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
  *           mx_quantize_nvfp4 took and wrote them (any number of rows).
  *  x        device, M x K, ldx elements per row, type xdt; 16-byte aligned,
  *           ldx * sizeof(elem) a multiple of 16.
- *  y        device, M x N, ldy elements per row, type ydt.
+ *  y        device, M x N, ldy elements per row, type ydt; must not overlap the
+ *           inputs.
  *  K        a multiple of 32 (MXFP4) or 16 (NVFP4), else MX_ERR_SHAPE; K = 0
  *           gives zeros.  M at most 65536, N at most 2^31 - 1, K at most 2^24,
  *           scales below 4 GiB (MX_ERR_UNSUPPORTED).  Any M is right; mx_gemm is the
  *           faster call from a few dozen tokens on.
- * A NaN scale makes its block's products NaN; NaN and Inf in x go by IEEE
+ * fp32 activations count down to 2^-133 (the bits below are dropped).  A NaN
+ * scale makes its block's products NaN; NaN and Inf in x go by IEEE
  * rules (0 * Inf is NaN).
  * Errors: MX_ERR_ARG, MX_ERR_ALIGN, MX_ERR_SHAPE, MX_ERR_UNSUPPORTED,
  * MX_ERR_CUDA.

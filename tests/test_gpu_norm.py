@@ -355,6 +355,48 @@ def test_graph_and_streams():
     assert not torch.equal(again[0], want[0])
 
 
+DEBUG_CALLS = """
+import sys, pickle, torch
+sys.path.insert(0, {root!r})
+from microscaling_block_scaled_mx_b200 import mx
+mx.LIB_PATH = {lib!r}
+g = torch.Generator(device="cuda").manual_seed(5)
+x = torch.randn(133, 1056, generator=g, device="cuda").bfloat16()
+w = torch.ones(1056, device="cuda")
+out = []
+for fmt in ("e4m3", "e2m3", "e2m1", "int8"):
+    for layout in ("plain", "mma", "mma_x4"):
+        u8 = dict(dtype=torch.uint8, device="cuda")
+        codes = torch.full((133, mx.codes_row_bytes(fmt, 1056)), 0xAB, **u8)
+        scales = torch.full((mx.scales_bytes(layout, 133, 1056),), 0xAB, **u8)
+        mx.rmsnorm_quantize(x, w, fmt=fmt, scale_layout=layout, out=(codes, scales, None, None, None))
+        out += [codes.cpu().numpy(), scales.cpu().numpy()]
+torch.cuda.synchronize()
+pickle.dump((mx.last_device_status(), out), open({path!r}, "wb"))
+"""
+
+
+def test_debug_build_gives_the_same(tmp_path):
+    """The bounds-checking build writes the same bytes and reports nothing."""
+    import os
+    import pickle
+    import subprocess
+    import sys
+
+    from microscaling_block_scaled_mx_b200 import build as B
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    got = []
+    for k, lib in enumerate((B.LIB, B.build(debug=True))):
+        path = str(tmp_path / f"{k}.pkl")
+        r = subprocess.run([sys.executable, "-c", DEBUG_CALLS.format(root=root, lib=lib, path=path)],
+                           capture_output=True, text=True, timeout=600)
+        assert r.returncode == 0, r.stderr[-2000:]
+        got.append(pickle.load(open(path, "rb")))
+    assert got[0][0] == 0 and got[1][0] == 0
+    for a, b in zip(got[0][1], got[1][1]):
+        assert np.array_equal(a, b)
+
+
 def test_offsets_past_32_bits(oracle):
     """More than 2^32 bytes and 2^31 values: the last rows are right."""
     rows, cols = 70000, 32768
