@@ -368,10 +368,14 @@ def gemm_quantize(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.
 # decoding step makes these calls for every layer and token, and on tensors of
 # a few kilobytes the host's part is most of their time.
 
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _device(t: torch.Tensor, what: str) -> int:
     """The index of t's device, which has to be the current one."""
     device = t.get_device()
-    if device < 0 or device != torch.cuda.current_device():
+    if device < 0 or device != _current_device():
         raise ValueError(f"{what} must be on the current CUDA device")
     return device
 
@@ -446,7 +450,7 @@ def _scale_bytes(layout: int, outer: int, blocks: int) -> int:
 
 def _handle(stream, device: int) -> int:
     """The stream's handle; of the current stream without a Stream object."""
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
 def _ptr(t) -> int | None:
