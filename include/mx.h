@@ -529,6 +529,74 @@ MX_API int mx_gemv_nvfp4(const void *w_codes, const void *w_scales, const float 
                          mx_scale_layout sl, const void *x, mx_dtype xdt, int64_t ldx, int64_t M, int64_t N,
                          int64_t K, float alpha, void *y, mx_dtype ydt, int64_t ldy, void *stream);
 
+/*
+ * mx_rmsnorm_packed, mx_rmsnorm_backward_packed, mx_gemv_packed -- the calls
+ * above with their arguments in one record of 8-byte fields, for bindings that
+ * pay for every argument of a foreign call (ctypes: 0.5 us instead of 2, of the
+ * 7 that a call for one token takes on the host).  `args` is a host pointer,
+ * of any alignment; it is read before the call returns.
+ *  mx_rmsnorm_args   cast != 0: mx_rmsnorm_quantize, else mx_rmsnorm (codes,
+ *                    scales, fmt, rnd, seed and sl are then not looked at).
+ *  mx_gemv_args      nvfp4 != 0: mx_gemv_nvfp4 (fw is not looked at), else
+ *                    mx_gemv (w_enc and w_domain_rows are not looked at).
+ * Results, checks and errors are those of the calls they stand for; a field
+ * that does not fit its argument's type is MX_ERR_ARG; so is a NULL args.
+ */
+typedef struct {
+    const void *x;
+    int64_t xdt, rows, cols, ldx;
+    const void *residual;
+    int64_t ldr;
+    const void *weight;
+    int64_t wdt;
+    double eps;
+    int64_t cast, fmt, rnd;
+    uint64_t seed;
+    void *h;
+    int64_t ldh;
+    void *y;
+    int64_t ldy;
+    float *rstd;
+    void *codes, *scales;
+    int64_t sl;
+    void *stream;
+} mx_rmsnorm_args;
+
+typedef struct {
+    const void *dy;
+    int64_t xdt, rows, cols, lddy;
+    const void *h;
+    int64_t ldh;
+    const void *weight;
+    int64_t wdt;
+    const float *rstd;
+    const void *dres;
+    int64_t lddres;
+    void *dx;
+    int64_t lddx;
+    float *dweight;
+    void *workspace;
+    int64_t ws_bytes;
+    void *stream;
+} mx_rmsnorm_backward_args;
+
+typedef struct {
+    const void *w_codes, *w_scales;
+    int64_t nvfp4, fw;
+    const float *w_enc;
+    int64_t w_domain_rows, sl;
+    const void *x;
+    int64_t xdt, ldx, M, N, K;
+    double alpha;
+    void *y;
+    int64_t ydt, ldy;
+    void *stream;
+} mx_gemv_args;
+
+MX_API int mx_rmsnorm_packed(const void *args);
+MX_API int mx_rmsnorm_backward_packed(const void *args);
+MX_API int mx_gemv_packed(const void *args);
+
 /* Byte sizes of the buffers above (0 for invalid arguments). */
 MX_API size_t mx_codes_bytes(mx_fmt fmt, int64_t outer, int64_t inner);
 MX_API size_t mx_scales_bytes(mx_scale_layout sl, int64_t outer, int64_t inner);

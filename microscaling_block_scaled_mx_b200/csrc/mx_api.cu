@@ -517,6 +517,9 @@ constexpr int64_t kMaxGrid = 2147483647;
 // size and the order of the sums depend on the sizes alone.
 int64_t norm_parts(int64_t rows) { return rows < 296 ? rows : 296; }
 
+// A packed field that may be cast to one of the enumerations.
+bool small(int64_t v) { return v >= 0 && v < 64; }
+
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // A matrix of `cols` values of type dt per row: MX_OK, or what is wrong.
@@ -684,6 +687,45 @@ int mx_gemv_nvfp4(const void *w_codes, const void *w_scales, const float *w_enc,
     const NvtxRange nvtx_range("mx_gemv_nvfp4");
     return gemv_impl(w_codes, w_scales, sl, true, w_enc, w_domain_rows, x, xdt, ldx, M, N, K, alpha, y, ydt, ldy,
                      stream);
+}
+
+int mx_rmsnorm_packed(const void *args) {
+    mx_rmsnorm_args a;
+    if (!args) return MX_ERR_ARG;
+    std::memcpy(&a, args, sizeof a);
+    if (!small(a.xdt) || !small(a.wdt)) return MX_ERR_ARG;
+    if (!a.cast)
+        return mx_rmsnorm(a.x, static_cast<mx_dtype>(a.xdt), a.rows, a.cols, a.ldx, a.residual, a.ldr, a.weight,
+                          static_cast<mx_dtype>(a.wdt), static_cast<float>(a.eps), a.h, a.ldh, a.y, a.ldy, a.rstd, a.stream);
+    if (!small(a.fmt) || !small(a.rnd) || !small(a.sl)) return MX_ERR_ARG;
+    return mx_rmsnorm_quantize(a.x, static_cast<mx_dtype>(a.xdt), a.rows, a.cols, a.ldx, a.residual, a.ldr, a.weight,
+                               static_cast<mx_dtype>(a.wdt), static_cast<float>(a.eps), static_cast<mx_fmt>(a.fmt),
+                               static_cast<mx_round>(a.rnd), a.seed, a.h, a.ldh, a.y, a.ldy, a.rstd, a.codes, a.scales,
+                               static_cast<mx_scale_layout>(a.sl), a.stream);
+}
+
+int mx_rmsnorm_backward_packed(const void *args) {
+    mx_rmsnorm_backward_args a;
+    if (!args) return MX_ERR_ARG;
+    std::memcpy(&a, args, sizeof a);
+    if (!small(a.xdt) || !small(a.wdt) || a.ws_bytes < 0) return MX_ERR_ARG;
+    return mx_rmsnorm_backward(a.dy, static_cast<mx_dtype>(a.xdt), a.rows, a.cols, a.lddy, a.h, a.ldh, a.weight,
+                               static_cast<mx_dtype>(a.wdt), a.rstd, a.dres, a.lddres, a.dx, a.lddx, a.dweight, a.workspace,
+                               static_cast<size_t>(a.ws_bytes), a.stream);
+}
+
+int mx_gemv_packed(const void *args) {
+    mx_gemv_args a;
+    if (!args) return MX_ERR_ARG;
+    std::memcpy(&a, args, sizeof a);
+    if (!small(a.fw) || !small(a.sl) || !small(a.xdt) || !small(a.ydt)) return MX_ERR_ARG;
+    if (a.nvfp4)
+        return mx_gemv_nvfp4(a.w_codes, a.w_scales, a.w_enc, a.w_domain_rows, static_cast<mx_scale_layout>(a.sl), a.x,
+                             static_cast<mx_dtype>(a.xdt), a.ldx, a.M, a.N, a.K, static_cast<float>(a.alpha), a.y,
+                             static_cast<mx_dtype>(a.ydt), a.ldy, a.stream);
+    return mx_gemv(a.w_codes, a.w_scales, static_cast<mx_fmt>(a.fw), static_cast<mx_scale_layout>(a.sl), a.x,
+                   static_cast<mx_dtype>(a.xdt), a.ldx, a.M, a.N, a.K, static_cast<float>(a.alpha), a.y,
+                   static_cast<mx_dtype>(a.ydt), a.ldy, a.stream);
 }
 
 int mx_last_device_status(void *stream) {

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -101,22 +102,11 @@ def lib() -> ctypes.CDLL:
             L.mx_gemm_quantize.restype = i32
             L.mx_gemm_quantize.argtypes = [vp, vp, i32, vp, vp, i32, i64, i64, i64, ctypes.c_float,
                                            i32, i32, u64, vp, vp, i32, vp]
-            L.mx_rmsnorm.restype = i32
-            L.mx_rmsnorm.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, ctypes.c_float, vp, i64, vp, i64,
-                                     vp, vp]
-            L.mx_rmsnorm_quantize.restype = i32
-            L.mx_rmsnorm_quantize.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, ctypes.c_float, i32, i32,
-                                              u64, vp, i64, vp, i64, vp, vp, vp, i32, vp]
-            L.mx_rmsnorm_backward.restype = i32
-            L.mx_rmsnorm_backward.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, vp, vp, i64, vp, i64, vp,
-                                              vp, ctypes.c_size_t, vp]
+            for name in ("mx_rmsnorm_packed", "mx_rmsnorm_backward_packed", "mx_gemv_packed"):
+                getattr(L, name).restype = i32
+                getattr(L, name).argtypes = [ctypes.c_char_p]
             L.mx_rmsnorm_backward_workspace_bytes.restype = ctypes.c_size_t
             L.mx_rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
-            L.mx_gemv.restype = i32
-            L.mx_gemv.argtypes = [vp, vp, i32, i32, vp, i32, i64, i64, i64, i64, ctypes.c_float, vp, i32, i64, vp]
-            L.mx_gemv_nvfp4.restype = i32
-            L.mx_gemv_nvfp4.argtypes = [vp, vp, vp, i64, i32, vp, i32, i64, i64, i64, i64, ctypes.c_float, vp, i32,
-                                        i64, vp]
             L.mx_codes_bytes.restype = ctypes.c_size_t
             L.mx_codes_bytes.argtypes = [i32, i64, i64]
             L.mx_scales_bytes.restype = ctypes.c_size_t
@@ -368,6 +358,12 @@ def gemm_quantize(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.
 # decoding step makes these calls for every layer and token, and on tensors of
 # a few kilobytes the host's part is most of their time.
 
+# The records of mx_rmsnorm_packed, mx_rmsnorm_backward_packed and mx_gemv_packed
+# (include/mx.h): addresses, numbers and two doubles, eight bytes each.
+_NORM_RECORD = struct.Struct("=Q4qQqQqd3qQQqQqQQQqQ").pack
+_BACKWARD_RECORD = struct.Struct("=Q4qQqQqQQqQqQQqQ").pack
+_GEMV_RECORD = struct.Struct("=QQqqQqqQ5qdQqqQ").pack
+
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -453,10 +449,6 @@ def _handle(stream, device: int) -> int:
     return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
-def _ptr(t) -> int | None:
-    return None if t is None else t.data_ptr()
-
-
 def _norm_args(x, weight, residual, h, y, want_y, rstd, want_rstd, stream):
     """Checks and allocations that the norm's two forms share."""
     dev, xdt, shape, ldx = _first(x, "x")
@@ -468,8 +460,7 @@ def _norm_args(x, weight, residual, h, y, want_y, rstd, want_rstd, stream):
         y = _empty(shape, x.dtype, x, stream)
     if want_rstd and rstd is None:
         rstd = _empty((rows,), torch.float32, x, stream)
-    r = hp = yp = rp = None
-    ldr = ldh = ldy = 0
+    r = hp = yp = rp = ldr = ldh = ldy = 0
     if residual is not None:
         ldr = _matrix(dev, residual, "residual", shape, x.dtype)
         ldh = _matrix(dev, h, "h", shape, x.dtype)
@@ -495,7 +486,7 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: 
     and y may be x."""
     y, h, rstd = out if out is not None else (None, None, None)
     ins, outs, dev, h, y, rstd = _norm_args(x, weight, residual, h, y, True, rstd, with_rstd, stream)
-    rc = (_lib or lib()).mx_rmsnorm(*ins, eps, *outs, _handle(stream, dev))
+    rc = (_lib or lib()).mx_rmsnorm_packed(_NORM_RECORD(*ins, eps, 0, 0, 0, 0, *outs, 0, 0, 0, _handle(stream, dev)))
     if rc != MX_OK:
         raise MxError(rc, "mx_rmsnorm")
     return y, h, rstd
@@ -523,8 +514,8 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
         scales = _empty(max(n_scales, 1), torch.uint8, x, stream)
     c = _flat(dev, codes, "codes", rows * row_bytes, torch.uint8)
     s = _flat(dev, scales, "scales", n_scales, torch.uint8)
-    rc = L.mx_rmsnorm_quantize(*ins, eps, f, ROUND[rnd] if isinstance(rnd, str) else int(rnd), seed & (2**64 - 1),
-                               *outs, c, s, sl, _handle(stream, dev))
+    rc = L.mx_rmsnorm_packed(_NORM_RECORD(*ins, eps, 1, f, ROUND[rnd] if isinstance(rnd, str) else int(rnd),
+                                          seed & (2**64 - 1), *outs, c, s, sl, _handle(stream, dev)))
     if rc != MX_OK:
         raise MxError(rc, "mx_rmsnorm_quantize")
     return codes, scales, h, y, rstd
@@ -559,8 +550,9 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rs
     rp = _flat(dev, rstd, "rstd", rows, torch.float32)
     dwp = _flat(dev, dweight, "dweight", cols, torch.float32)
     wsp = _flat(dev, workspace, "workspace", n_ws, torch.uint8)
-    rc = L.mx_rmsnorm_backward(dy.data_ptr(), dt, rows, cols, lddy, h.data_ptr(), ldh, w, wdt, rp, _ptr(dres),
-                               lddres, dx.data_ptr(), lddx, dwp, wsp, workspace.numel(), _handle(stream, dev))
+    rc = L.mx_rmsnorm_backward_packed(_BACKWARD_RECORD(
+        dy.data_ptr(), dt, rows, cols, lddy, h.data_ptr(), ldh, w, wdt, rp, 0 if dres is None else dres.data_ptr(), lddres,
+        dx.data_ptr(), lddx, dwp, wsp, workspace.numel(), _handle(stream, dev)))
     if rc != MX_OK:
         raise MxError(rc, "mx_rmsnorm_backward")
     return dx, dweight
@@ -599,7 +591,7 @@ def gemv(w_codes: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, N: int,
     L = _lib or lib()
     c = _flat(dev, w_codes, "w_codes", N * K // 2, torch.uint8)
     s = _flat(dev, w_scales, "w_scales", _scale_bytes(sl, N, -(-K // 32)), torch.uint8)
-    rc = L.mx_gemv(c, s, f, sl, *ins, alpha, *outs, _handle(stream, dev))
+    rc = L.mx_gemv_packed(_GEMV_RECORD(c, s, 0, f, 0, 0, sl, *ins, alpha, *outs, _handle(stream, dev)))
     if rc != MX_OK:
         raise MxError(rc, "mx_gemv")
     return out
@@ -618,7 +610,7 @@ def gemv_nvfp4(w, x: torch.Tensor, N: int, K: int, domain_rows: int = 0, alpha: 
     s = _flat(dev, scales, "scales", _scale_bytes(sl, N, -(-K // 16)), torch.uint8)
     domains = -(-N // domain_rows) if domain_rows > 0 else 1         # a negative one is refused by the call
     e = _flat(dev, enc, "enc_scales", domains, torch.float32)
-    rc = L.mx_gemv_nvfp4(c, s, e, domain_rows, sl, *ins, alpha, *outs, _handle(stream, dev))
+    rc = L.mx_gemv_packed(_GEMV_RECORD(c, s, 1, 0, e, domain_rows, sl, *ins, alpha, *outs, _handle(stream, dev)))
     if rc != MX_OK:
         raise MxError(rc, "mx_gemv_nvfp4")
     return out

@@ -6,8 +6,19 @@ import torch
 
 @pytest.fixture(scope="module")
 def mx():
+    import ctypes
+
     from microscaling_block_scaled_mx_b200 import build, mx as m
     build.build()
+    L = m.lib()                         # the binding itself calls the packed forms
+    vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    L.mx_rmsnorm.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, f32, vp, i64, vp, i64, vp, vp]
+    L.mx_rmsnorm_quantize.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, f32, i32, i32, ctypes.c_uint64, vp,
+                                      i64, vp, i64, vp, vp, vp, i32, vp]
+    L.mx_rmsnorm_backward.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, vp, vp, i64, vp, i64, vp, vp,
+                                      ctypes.c_size_t, vp]
+    L.mx_gemv.argtypes = [vp, vp, i32, i32, vp, i32, i64, i64, i64, i64, f32, vp, i32, i64, vp]
+    L.mx_gemv_nvfp4.argtypes = [vp, vp, vp, i64, i32, vp, i32, i64, i64, i64, i64, f32, vp, i32, i64, vp]
     return m
 
 
@@ -98,6 +109,32 @@ def test_gemv_nvfp4_refusals(mx):
 
     assert call(K=24) == -3 and call(dom=-1) == -1 and call(enc=None) == -1 and call(enc=18) == -2
     assert call(sl=3) == -1 and call(scales=8) == -2 and call(M=0, enc=None) == 0
+
+
+def test_packed_refusals(mx):
+    """A record goes through the same checks; fields out of their types' range are refused."""
+    L = mx.lib()
+    norm = [16, 1, 4, 64, 64, 0, 0, 16, 1, 1e-5, 0, 0, 0, 0, 0, 0, 16, 64, 0, 0, 0, 0, 0]
+    back = [16, 1, 4, 64, 64, 16, 64, 16, 1, 16, 0, 0, 16, 64, 16, 16, 4 * 64 * 4, 0]
+    gemv = [16, 16, 0, 4, 0, 0, 1, 16, 1, 256, 1, 64, 256, 1.0, 16, 1, 64, 0]
+
+    def call(name, record, pack, **change):
+        r = list(record)
+        for k, v in change.items():
+            r[int(k[1:])] = v
+        return getattr(L, name)(pack(*r))
+
+    n = lambda **c: call("mx_rmsnorm_packed", norm, mx._NORM_RECORD, **c)            # noqa: E731
+    b = lambda **c: call("mx_rmsnorm_backward_packed", back, mx._BACKWARD_RECORD, **c)   # noqa: E731
+    v = lambda **c: call("mx_gemv_packed", gemv, mx._GEMV_RECORD, **c)               # noqa: E731
+    assert L.mx_rmsnorm_packed(None) == L.mx_rmsnorm_backward_packed(None) == L.mx_gemv_packed(None) == -1
+    assert n(_0=0) == -1 and n(_1=2 ** 32 + 1) == -1 and n(_3=48) == -3 and n(_0=8) == -2 and n(_2=0) == 0
+    assert n(_10=1) == -1 and n(_10=1, _19=16, _20=16, _21=2 ** 32) == -1 and n(_10=1, _19=24, _20=16, _21=1) == -2
+    assert n(_10=1, _19=16, _20=16, _11=-1) == -1 and n(_16=0) == -1 and n(_14=16) == -1 and n(_9=1e300) == -1
+    assert b(_0=0) == -1 and b(_16=4 * 64 * 4 - 1) == -1 and b(_16=-1) == -1 and b(_14=2) == -2 and b(_3=48) == -3
+    assert b(_3=0, _0=0) == 0 and b(_8=2 ** 32) == -1
+    assert v(_3=0) == -4 and v(_3=2 ** 33 + 4) == -1 and v(_12=48) == -3 and v(_0=8) == -2 and v(_10=0) == 0
+    assert v(_2=1) == -1 and v(_2=1, _4=18) == -2 and v(_2=1, _4=16, _12=24) == -3 and v(_15=2) == -1
 
 
 def test_binding_refuses_before_the_library(mx):
