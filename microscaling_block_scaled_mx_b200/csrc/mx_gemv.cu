@@ -86,6 +86,19 @@ __device__ __forceinline__ void copy_async_part(uint32_t dst, const void *src, u
     asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(B) : "memory");
 }
 
+// Plain loads, in their place: the preceding kernel may still write when this one
+// starts, which the read-only path does not allow for.
+__device__ __forceinline__ uint4 load16(const void *src) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t load_byte(const uint8_t *src) {
+    uint32_t v;
+    asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(src) : "memory");
+    return v;
+}
+
 // 16 x 8 x 16 products; FIRST: the sum starts from zero.
 template <bool BF16, bool FIRST>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -384,7 +397,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
                 copy_async_part<4>(sdst + slot + i * 128, n ? from : p.scales, n);
             } else {
 #pragma unroll
-                for (uint32_t j = 0; j < 4; ++j) bytes[BYTES ? i : 0][j] = j < n ? __ldg(from + j) : 0u;
+                for (uint32_t j = 0; j < 4; ++j) bytes[BYTES ? i : 0][j] = j < n ? load_byte(from + j) : 0u;
             }
         }
         advance();
@@ -429,8 +442,8 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
                 for (int h = 0; h < (XF32 ? 2 : 1); ++h) {
                     v[b][h] = make_uint4(0, 0, 0, 0);
                     if (in)
-                        v[b][h] = XF32 ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(p.x) + off) + h)
-                                       : __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + off));
+                        v[b][h] = XF32 ? load16(static_cast<const float *>(p.x) + off + 4 * h)
+                                       : load16(static_cast<const uint16_t *>(p.x) + off);
                 }
                 to[b] = tok * pitch + j * (SLICE * 2) + lane * 16;
                 flag[b] = j * (8 * NT) + tok;
@@ -559,9 +572,20 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
         const uint32_t ti = e / rows, c = (e - ti * rows) / 16, q = e % 16, at = tile_lo + c;
         const float *theirs = reinterpret_cast<const float *>(smem + c * S::RING) + ti * 16 + q;
         float v = 0.0f;
-        for (uint32_t r = 0; r < size; ++r) {
-            const float *from = size > 1 ? cg::this_cluster().map_shared_rank(theirs, r) : theirs;
-            for (uint32_t k = 0; k < p.share; ++k) v += from[k * p.lanes * (S::RING / 4)];
+        if (size == 1) {
+            for (uint32_t k = 0; k < p.parts; ++k) v += theirs[k * p.lanes * (S::RING / 4)];
+        } else {
+            for (uint32_t k = 0; k < p.parts; k += 4) {        // in order, four loads in flight
+                float f[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t one = min(k + j, p.parts - 1), r = small_quotient(one, p.share_inv);
+                    f[j] = *cg::this_cluster().map_shared_rank(theirs + (one - r * p.share) * p.lanes * (S::RING / 4), r);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (k + j < p.parts) v += f[j];
+            }
         }
         const uint32_t row = at / 8 * ATOM + 4 * (at % 8) + (q & 3u) + 64 * ((q >> 2) & 1u) + 32 * (q >> 3);
         store_y<NV>(p, t0 + ti, row, v);
@@ -674,8 +698,7 @@ cudaError_t launch_kernel(GemvParams &p, int sms, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = size > 1 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kern, p);
-    return e == cudaSuccess ? cudaGetLastError() : e;
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <bool XF32, bool NV, int NT>

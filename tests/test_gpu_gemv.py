@@ -136,12 +136,13 @@ def test_tokens_are_independent():
 
 
 @pytest.mark.parametrize("N,K", [(300, 8192), (4100, 4096), (40, 14336)])
-def test_a_batch_of_any_size_gives_the_same(N, K):
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_batch_of_any_size_gives_the_same(N, K, dtype):
     """The work is cut differently for one token and for sixteen, the sums are not;
     and a token whose neighbours need bf16 products keeps its bits."""
     codes, scales, _ = mx_weights(N, K, "mma", 40)
     ws, _ = nv_weights(N, K, "mma_x4", 0, 41)
-    x = activations(24, K, torch.bfloat16, 42)
+    x = activations(24, K, dtype, 42)
     x[5, 3] = 5000.0                                # past what fp16 takes, in the first slice
     x[17, K - 1] = 1e-12                            # below it, in the last
     x[20] *= 2.0 ** -60
@@ -409,3 +410,22 @@ def test_a_decoding_step():
     assert np.all(np.abs(f64(c) - a @ w.T) <= 1e-5 * (np.abs(a) @ np.abs(w).T) + 1e-30)
     torch.cuda.synchronize()
     assert mx.last_device_status() == 0
+
+
+@pytest.mark.parametrize("N", [28416, 19000])
+def test_two_and_three_parts_of_k(N):
+    """Sizes whose K is cut in two or three: sixteen tokens, whose two parts a
+    cluster shares, have the bits of one, which is checked against the product."""
+    K = 2304
+    g = torch.Generator(device=dev()).manual_seed(50)
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=dev(), generator=g)
+    scales = torch.randint(118, 130, (N, K // 32), dtype=torch.uint8, device=dev(), generator=g)
+    x = activations(16, K, torch.bfloat16, 51)
+    y = mx.gemv(codes, scales, x, N, K, scale_layout="plain", out_dtype=torch.float32)
+    assert all(torch.equal(y[i:i + 1], mx.gemv(codes, scales, x[i:i + 1], N, K, scale_layout="plain",
+                                               out_dtype=torch.float32)) for i in (0, 7, 15))
+    pick = [0, 1, 127, 128, N // 2, N - 130, N - 1]
+    c, s = codes[pick].cpu().numpy(), scales[pick].cpu().numpy()
+    w = np.empty((len(pick), K))
+    w[:, 0::2], w[:, 1::2] = VALUES[c & 15], VALUES[c >> 4]
+    check(y[:, pick], x, w * np.repeat(np.exp2(s.astype(np.float64) - 127), 32, axis=1))
