@@ -432,8 +432,8 @@ MX_API int mx_gemm_quantize_x4(const void *a_codes, const void *a_scales, mx_fmt
  *    y_c  = (h_c * rstd) * weight_c
  * The sum of squares is fp32 in an order fixed by cols and xdt; every other
  * step is one IEEE fp32 operation (the inverse square root and 1 / cols are
- * each rounded once), so a row's result does not depend on the other rows.  The squares overflow fp32 for |h| above
- * 1.8e19: rstd is then 0.  A NaN in h makes its whole row of y NaN; an Inf
+ * each rounded once), so a row's result does not depend on the other rows.
+ * The squares overflow fp32 for |h| above 1.8e19: rstd is then 0.  A NaN in h makes its whole row of y NaN; an Inf
  * makes rstd 0, and y is NaN at the Inf and zero elsewhere.
  *
  *  x        device, rows x cols, ldx elements per row, type xdt; 16-byte
@@ -514,8 +514,8 @@ MX_API size_t mx_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
  *           inputs.
  *  K        a multiple of 32 (MXFP4) or 16 (NVFP4), else MX_ERR_SHAPE; K = 0
  *           gives zeros.  M at most 65536, N at most 2^31 - 1, K at most 2^24,
- *           scales below 4 GiB (MX_ERR_UNSUPPORTED).  Any M is right; mx_gemm is the
- *           faster call from a few dozen tokens on.
+ *           scales below 4 GiB (MX_ERR_UNSUPPORTED).  Any M is right; mx_gemm
+ *           is the faster call from a few dozen tokens on.
  * fp32 activations count down to 2^-133 (the bits below are dropped).  A NaN
  * scale makes its block's products NaN; NaN and Inf in x go by IEEE
  * rules (0 * Inf is NaN).

@@ -10,6 +10,7 @@
 //   dx = rstd * (a - n * sum(a n) / cols) + dres
 //   dweight = sum over rows of dy * n
 #include <algorithm>
+#include <cooperative_groups.h>
 #include <cstdint>
 #include <type_traits>
 #include <cuda_bf16.h>
@@ -22,6 +23,7 @@
 namespace mxnorm {
 
 using namespace mxk;
+namespace cg = cooperative_groups;
 
 struct NormParams {
     const void *x, *res;
@@ -317,6 +319,11 @@ __device__ __forceinline__ void cast_as(const NormParams &p, int64_t row, uint32
 // eight values, vector i of thread t being i * blockDim + t (so four
 // neighbouring lanes hold a block), and the weight's of the same columns.
 // Vectors past the row's end are zero, like their weights, and not stored.
+// Memory bounds it: a bf16 row with a residual moves 4 bytes a value in, 2 of h
+// out, and 2 of y or 1 + 1/32 of E4M3 codes.  Measured (16384 x 4096 bf16):
+// 88 us, 6.1 TB/s, with y, and 83 us, 5.7 TB/s, with codes (a copy makes 6.5;
+// the cast's instructions fill half of the issue slots); 8192 x 4096 fp32 with
+// codes 73 us, 6.0 TB/s; one row of 4096 1.8 us, a chain of latencies.
 template <bool BF16, bool RES, int V, int T, int CAST>
 __global__ void __launch_bounds__(T, 1) norm_kernel(const __grid_constant__ NormParams p) {
     // the next row's loads are in flight while this one is worked on, where registers allow
@@ -435,7 +442,8 @@ struct BackParams {
     float *dw, *part;
     uint32_t parts;
     float inv_cols;
-    uint32_t threads, groups;  // threads to a row, rows of a CTA at a time
+    uint32_t cluster, each;    // CTAs that share a row, and the pieces of each (the last has the rest)
+    uint32_t threads, groups;  // threads to a CTA's share of a row, rows of a CTA at a time
     int stages;                // rows in each group's ring
 };
 
@@ -500,38 +508,59 @@ __device__ __forceinline__ float group_sum(float s, float *red, uint32_t warps, 
     return (t.x + t.y) + (t.z + t.w);
 }
 
-// Group k of CTA b takes rows b * groups + k, and every gridDim * groups rows
-// from there; a thread has V pieces of a row, piece i * threads + t.  It keeps
-// its columns' share of dweight in registers; at the end the groups' shares are
-// added in order and written to part[b].
-// STAGED: the rows pass through a ring of p.stages rows in shared memory, where
-// each thread copies its own columns ahead of their use and reads them twice
-// (no other thread does, so the ring needs no barrier); else a row is read
-// twice from global memory.
-template <bool BF16, bool RES, int V, bool STAGED>
-__global__ void __launch_bounds__(STAGED || BF16 ? 512 : 1024, 1) norm_backward_kernel(const __grid_constant__ BackParams p) {
+// Sum over the cluster, in the CTAs' order; every thread has its CTA's sum s and
+// gets the cluster's.  `all` is the same place in every CTA, and not the last
+// row's: a CTA may still read that one.
+__device__ __forceinline__ float cluster_sum(float s, float *all, uint32_t cluster, uint32_t rank) {
+    if (threadIdx.x < cluster) *cg::this_cluster().map_shared_rank(all + rank, threadIdx.x) = s;
+    cg::this_cluster().sync();
+    s = all[0];
+    for (uint32_t i = 1; i < cluster; ++i) s += all[i];
+    return s;
+}
+
+// WIDE: a row is shared by the CTAs of a cluster, each with its own columns.
+// Cluster b (else CTA b) takes rows b * groups to b * groups +
+// groups - 1, group k of the CTA the kth, and every parts * groups rows from
+// there; a thread has V pieces of its CTA's share of a row, piece i * threads + t.
+// It keeps its columns' share of dweight in registers; at the end the groups'
+// shares are added in order and written to part[b].
+// The rows pass through a ring of p.stages rows in shared memory, where each
+// thread copies its own columns ahead of their use and reads them twice (no
+// other thread does, so the ring needs no barrier).  Registers for the next row
+// instead: 51.5 us against 48 at 8192 x 4096 bf16; rows read twice from global
+// memory: 308.
+// Memory bounds it: dy, h and dres in, dx out, 8 bytes a bf16 value, and behind
+// that the wait for each row's sum.  Measured, dweight's kernel of 3 to 4 us
+// included: 16384 x 4096 bf16 85 us, 6.3 TB/s; 8192 x 4096 bf16 49 us, 5.5 TB/s,
+// and fp32 85 us, 6.3 TB/s.
+template <bool BF16, bool RES, int V, bool WIDE>
+__global__ void __launch_bounds__(512, 1) norm_backward_kernel(const __grid_constant__ BackParams p) {
     using P = Piece<BF16>;
     constexpr int ARRAYS = RES ? 3 : 2;
     after_predecessor();
     __shared__ __align__(16) float red[2][32];
+    __shared__ float across[WIDE ? 2 : 1][4];
     extern __shared__ __align__(16) uint4 ring[];              // [group][stage][array][piece]
     const uint32_t n = p.threads, group = threadIdx.x / n, t = threadIdx.x - group * n;
     const uint32_t warps = n / 32, warp = t >> 5, row_vecs = V * n, stage_vecs = ARRAYS * row_vecs;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * p.groups + group, step = static_cast<int64_t>(gridDim.x) * p.groups;
+    const uint32_t rank = WIDE ? blockIdx.x % p.cluster : 0u, block = WIDE ? blockIdx.x / p.cluster : blockIdx.x;
+    const uint32_t base = rank * p.each, pieces = WIDE ? min(p.each, p.pieces - base) : p.pieces;    // of this CTA
+    const int64_t first = static_cast<int64_t>(block) * p.groups + group, step = static_cast<int64_t>(WIDE ? p.parts : gridDim.x) * p.groups;
     constexpr int SIZE = BF16 ? 2 : 4;
-    const char *in[3] = {static_cast<const char *>(p.dy) + first * p.lddy * SIZE + 16 * t,
-                         static_cast<const char *>(p.h) + first * p.ldh * SIZE + 16 * t,
-                         RES ? static_cast<const char *>(p.dres) + first * p.lddres * SIZE + 16 * t : nullptr};
+    const char *in[3] = {static_cast<const char *>(p.dy) + first * p.lddy * SIZE + 16 * (base + t),
+                         static_cast<const char *>(p.h) + first * p.ldh * SIZE + 16 * (base + t),
+                         RES ? static_cast<const char *>(p.dres) + first * p.lddres * SIZE + 16 * (base + t) : nullptr};
     const int64_t by[3] = {step * p.lddy * SIZE, step * p.ldh * SIZE, RES ? step * p.lddres * SIZE : 0};
-    char *out = static_cast<char *>(p.dx) + first * p.lddx * SIZE + 16 * t;
+    char *out = static_cast<char *>(p.dx) + first * p.lddx * SIZE + 16 * (base + t);
     uint4 *mine = ring + group * p.stages * stage_vecs + t;
-    const uint32_t mine32 = STAGED ? static_cast<uint32_t>(__cvta_generic_to_shared(mine)) : 0u;
+    const uint32_t mine32 = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
     auto fetch = [&](uint32_t at) {                            // the next row to be read
 #pragma unroll
         for (int a = 0; a < ARRAYS; ++a) {
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (i * n + t < p.pieces)
+                if (i * n + t < pieces)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(mine32 + (at + a * row_vecs + i * n) * 16),
                                  "l"(in[a] + i * n * 16)
                                  : "memory");
@@ -539,19 +568,19 @@ __global__ void __launch_bounds__(STAGED || BF16 ? 512 : 1024, 1) norm_backward_
         }
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
-    if (STAGED)
-        for (int s = 0; s < p.stages - 1; ++s) {
-            if (first + s * step < p.rows) fetch(s * stage_vecs);
-            commit();
-        }
-    f2 acc[V][P::PAIRS], w[STAGED ? V : 1][P::PAIRS];
+    for (int s = 0; s < p.stages - 1; ++s) {
+        if (first + s * step < p.rows) fetch(s * stage_vecs);
+        commit();
+    }
+    f2 acc[V][P::PAIRS], w[V][P::PAIRS];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
         for (int j = 0; j < P::PAIRS; ++j) acc[i][j] = 0;
-        if (STAGED && i * n + t < p.pieces) P::weights(p.w, p.w_f32, (i * n + t) * P::VALUES, w[STAGED ? i : 0]);
+        if (i * n + t < pieces) P::weights(p.w, p.w_f32, (base + i * n + t) * P::VALUES, w[i]);
     }
     clear_sums(red);
+    if (WIDE) cg::this_cluster().sync();              // the others run: their shared memory can be written
     float rstd = first < p.rows ? p.rstd[first] : 0.0f;
     int turn = 0;
     const uint32_t last = (p.stages - 1) * stage_vecs, place = group * ((warps + 3) & ~3u);
@@ -559,36 +588,30 @@ __global__ void __launch_bounds__(STAGED || BF16 ? 512 : 1024, 1) norm_backward_
     for (int64_t row = first; row < p.rows; row += step, turn ^= 1) {
         const f2 rs = pair(rstd, rstd);
         if (row + step < p.rows) rstd = p.rstd[row + step];
-        if (STAGED) {
-            // this thread's copies of the row have landed (all but the last stages - 2 groups)
-            if (p.stages == 2) asm volatile("cp.async.wait_group 0;" ::: "memory");
-            else if (p.stages == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
-            else asm volatile("cp.async.wait_group 2;" ::: "memory");
-            if (row + (p.stages - 1) * step < p.rows) fetch(at == 0 ? last : at - stage_vecs);
-            commit();
-        }
-        auto get = [&](int a, int i, P &x) {
-            x.v = STAGED ? mine[at + a * row_vecs + i * n] : *reinterpret_cast<const uint4 *>(in[a] + i * n * 16);
-        };
+        // this thread's copies of the row have landed (all but the last stages - 2 groups)
+        if (p.stages == 2) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        else if (p.stages == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 2;" ::: "memory");
+        if (row + (p.stages - 1) * step < p.rows) fetch(at == 0 ? last : at - stage_vecs);
+        commit();
+        auto get = [&](int a, int i, P &x) { x.v = mine[at + a * row_vecs + i * n]; };
         // the piece's a = dy * weight and n = h * rstd, and dy
         auto terms = [&](int i, f2 (&a)[P::PAIRS], f2 (&nn)[P::PAIRS], f2 (&dy)[P::PAIRS]) {
             P g, h;
-            f2 wl[P::PAIRS];
             get(0, i, g);
             get(1, i, h);
-            if (!STAGED) P::weights(p.w, p.w_f32, (i * n + t) * P::VALUES, wl);
             g.widen(dy);
             h.widen(nn);
 #pragma unroll
             for (int j = 0; j < P::PAIRS; ++j) {
                 nn[j] = mul2(nn[j], rs);
-                a[j] = mul2(dy[j], STAGED ? w[STAGED ? i : 0][j] : wl[j]);
+                a[j] = mul2(dy[j], w[i][j]);
             }
         };
         f2 dot = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (i * n + t >= p.pieces) continue;
+            if (i * n + t >= pieces) continue;
             f2 a[P::PAIRS], nn[P::PAIRS], dy[P::PAIRS];
             terms(i, a, nn, dy);
 #pragma unroll
@@ -599,11 +622,13 @@ __global__ void __launch_bounds__(STAGED || BF16 ? 512 : 1024, 1) norm_backward_
         }
         float s0, s1;
         unpair(dot, s0, s1);
-        const float c = group_sum(s0 + s1, red[turn] + place, warps, warp, 1 + group) * p.inv_cols;
+        float c = group_sum(s0 + s1, red[turn] + place, warps, warp, 1 + group);
+        if (WIDE) c = cluster_sum(c, across[WIDE ? turn : 0], p.cluster, rank);
+        c *= p.inv_cols;
         const f2 minus_c = pair(-c, -c);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (i * n + t >= p.pieces) continue;
+            if (i * n + t >= pieces) continue;
             f2 a[P::PAIRS], nn[P::PAIRS], dy[P::PAIRS];
             terms(i, a, nn, dy);
 #pragma unroll
@@ -619,15 +644,10 @@ __global__ void __launch_bounds__(STAGED || BF16 ? 512 : 1024, 1) norm_backward_
             *reinterpret_cast<uint4 *>(out + i * n * 16) = o.v;
         }
         out += step * p.lddx * SIZE;
-        if (STAGED) {
-            at = at == last ? 0 : at + stage_vecs;
-        } else {
-#pragma unroll
-            for (int a = 0; a < ARRAYS; ++a) in[a] += by[a];
-        }
+        at = at == last ? 0 : at + stage_vecs;
     }
     // the groups' shares, through the ring (its copies have landed) and in order
-    float *part = p.part + static_cast<int64_t>(blockIdx.x) * p.cols;
+    float *part = p.part + static_cast<int64_t>(block) * p.cols;
     float *shares = reinterpret_cast<float *>(ring);
     if (p.groups > 1) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -635,8 +655,8 @@ __global__ void __launch_bounds__(STAGED || BF16 ? 512 : 1024, 1) norm_backward_
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        if (i * n + t >= p.pieces) continue;
-        float *to = (p.groups > 1 ? shares + group * p.cols : part) + (i * n + t) * P::VALUES;
+        if (i * n + t >= pieces) continue;
+        float *to = (p.groups > 1 ? shares + group * p.cols : part) + (base + i * n + t) * P::VALUES;
 #pragma unroll
         for (int j = 0; j < P::PAIRS; ++j) {
             float lo, hi;
@@ -654,7 +674,9 @@ __global__ void __launch_bounds__(STAGED || BF16 ? 512 : 1024, 1) norm_backward_
 }
 
 // dweight[c] = the sum of the parts: 32 columns to a CTA, warp w adds parts w,
-// w + 32, ..., and the warps' sums are added in their order.
+// w + 32, ..., and the warps' sums are added in their order.  No atomics, so the
+// result has one value; 296 parts x 4096 columns are 4.8 MB that the backward
+// kernel has just left in L2.
 constexpr int DW_WARPS = 32;
 __global__ void __launch_bounds__(32 * DW_WARPS) norm_dweight_kernel(const float *part, uint32_t parts, uint32_t cols, float *dw) {
     __shared__ float red[DW_WARPS][32];
@@ -673,17 +695,21 @@ __global__ void __launch_bounds__(32 * DW_WARPS) norm_dweight_kernel(const float
 
 // Launches a kernel that begins with after_predecessor().
 template <typename Kern, typename... Args>
-cudaError_t launch_early(Kern kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t st, const Args &...args) {
+cudaError_t launch_early(Kern kern, unsigned grid, unsigned cluster, unsigned threads, size_t smem, cudaStream_t st,
+                         const Args &...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
@@ -702,7 +728,7 @@ cudaError_t launch_norm(const NormParams &p, int sms, cudaStream_t st) {
     auto kern = norm_kernel<BF16, RES, V, T, CAST>;
     const int threads = threads_for(p.vecs, V);
     const int64_t most = p.rows <= sms ? p.rows : resident(kern, threads, sms);
-    return launch_early(kern, static_cast<unsigned>(p.rows < most ? p.rows : most), threads, 0, st, p);
+    return launch_early(kern, static_cast<unsigned>(p.rows < most ? p.rows : most), 1, threads, 0, st, p);
 }
 
 template <bool BF16, bool RES, int V, int T>
@@ -717,6 +743,17 @@ cudaError_t launch_norm_cast(const NormParams &p, int cast, int sms, cudaStream_
     }
 }
 
+// Vectors of a thread: few where a row has to be spread over many threads, more
+// where a wider CTA would only make the sum's barriers longer; 32 rows of a CTA's
+// threads are the most that keep several CTAs on an SM.  Measured (bf16 with
+// residual and E4M3 cast, us with V = 1, 2, 4):
+//   vecs   32   32768 x 256    11.0  16.1  24.4
+//   vecs  128   16384 x 1024   21.6  22.9  20.3
+//   vecs  132   1013 x 1056     4.8   5.4
+//   vecs  512   16384 x 4096   82    82    85
+//   vecs 1024   4096 x 8192          45.8  42.3
+// and fp32, vecs 512, 8192 x 4096: 76, 73, 76 to 82.  (vecs 64: not measured,
+// as between its neighbours.)
 template <bool BF16, bool RES>
 cudaError_t launch_norm_v(const NormParams &p, int cast, int sms, cudaStream_t st) {
     const int v = p.vecs <= 32 ? 1 : p.vecs <= 64 ? 2 : p.vecs <= 128 ? 4 : p.vecs <= 256 ? 1 : p.vecs <= (BF16 ? 512 : 1024) ? 2 : 4;
@@ -726,35 +763,55 @@ cudaError_t launch_norm_v(const NormParams &p, int cast, int sms, cudaStream_t s
     return launch_norm_cast<BF16, RES, 4, 1024>(p, cast, sms, st);
 }
 
-constexpr int BACK_SMEM = 226 * 1024;        // with the sums' 256 bytes, what a CTA can have
+constexpr int BACK_SMEM = 226 * 1024;        // with the sums' 288 bytes, what a CTA can have
 constexpr int BACK_HALF = 112 * 1024;        // two CTAs to an SM
+constexpr uint32_t BACK_THREADS = 512, BACK_V = 4;
 
-template <bool BF16, bool RES, int V>
-cudaError_t launch_staged(const BackParams &p, cudaStream_t st) {
+template <bool BF16, bool RES, int V, bool WIDE>
+cudaError_t launch_back(const BackParams &p, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    auto kern = norm_backward_kernel<BF16, RES, V, true>;
+    auto kern = norm_backward_kernel<BF16, RES, V, WIDE>;
     const cudaError_t e = ensure_smem_limit(kern, BACK_SMEM, done);
     if (e != cudaSuccess) return e;
-    return launch_early(kern, p.parts, p.threads * p.groups, p.groups * p.stages * (RES ? 3 : 2) * V * p.threads * 16, st, p);
+    return launch_early(kern, p.parts * p.cluster, p.cluster, p.threads * p.groups,
+                        p.groups * p.stages * (RES ? 3 : 2) * V * p.threads * 16, st, p);
 }
 
+// A row wider than the 2048 pieces that 512 threads of four hold is shared by a
+// cluster of two or four CTAs.  Pieces of a thread: as many as leave a row a CTA
+// of 256 threads, or several rows the threads of one.  Measured (us with V = 1,
+// 2, 4):
+//   pieces   32   32768 x 256  bf16   16.9  17.5  19.1
+//   pieces   64   16384 x 512  bf16   18.2  16.8  16.2
+//   pieces  128   16384 x 1024 bf16   30.7  28.6  28.7
+//   pieces  264   333 x 1056   fp32    7.7   7.5   6.5
+//   pieces  320   8192 x 2560  bf16   37.4  40.9  35.2
+//   pieces  448   8192 x 3584  bf16   61.3  44.4  44.9
+//   pieces  512   8192 x 4096  bf16   64.5  49.2  50.6
+//   pieces 1024   4096 x 8192  bf16         58.1  51.8
+// Threads of a CTA of several rows, 128, 256, 512 (and one row): 32768 x 256
+// 21.6, 16.7, 20.1 (54); 16384 x 1024 33.2, 29.0, 30.9 (43).
+// The ring has two to four rows of each group, in half of the shared memory if
+// they fit there: two CTAs to an SM, 2 x 148 parts, hide each other's sums (one
+// CTA: 8192 x 4096 59 us against 49).  Where the SM has one CTA at a time, more
+// than 148 parts would run one after the other (2048 x 16384 65 us against 54);
+// of clusters the device may hold somewhat fewer than 148 CTAs' worth.
 template <bool BF16, bool RES>
 cudaError_t launch_backward_v(BackParams &p, cudaStream_t st) {
-    const int v = p.pieces <= 64 ? 1 : p.pieces <= 512 ? 2 : 4;
-    p.threads = threads_for(p.pieces, v);
+    p.cluster = p.pieces <= BACK_V * BACK_THREADS ? 1 : p.pieces <= 2 * BACK_V * BACK_THREADS ? 2 : 4;    // cols <= 32768
+    p.each = (p.pieces + p.cluster - 1) / p.cluster;
+    const int v = p.pieces <= 32 ? 1 : p.pieces <= 384 || p.pieces > 512 ? 4 : 2;
+    p.threads = threads_for(p.each, v);
     p.groups = std::max(1u, 256 / p.threads);
-    const int row = p.groups * (RES ? 3 : 2) * v * p.threads * 16;       // bytes of a stage
-    if (p.threads <= 512 && 2 * row <= BACK_SMEM) {
-        p.stages = std::max(2, std::min(4, BACK_HALF / row));
-        p.parts = static_cast<uint32_t>(std::min<int64_t>((p.rows + p.groups - 1) / p.groups, p.parts));
-        if (v == 1) return launch_staged<BF16, RES, 1>(p, st);
-        if (v == 2) return launch_staged<BF16, RES, 2>(p, st);
-        return launch_staged<BF16, RES, 4>(p, st);
-    }
-    p.groups = 1;
-    p.stages = 0;
-    p.threads = threads_for(p.pieces, 8);                                // cols <= 32768: at most 1024 (fp32)
-    return launch_early(norm_backward_kernel<BF16, RES, 8, false>, p.parts, p.threads, 0, st, p);
+    const int row = p.groups * (RES ? 3 : 2) * v * p.threads * 16;       // bytes of a stage, 96 KB at most
+    p.stages = std::max(2, std::min(4, BACK_HALF / row));
+    if (p.cluster > 1) p.parts = std::min(p.parts, p.cluster == 2 ? 72u : 32u);
+    else if (p.stages * row > BACK_HALF) p.parts = std::min(p.parts, 148u);
+    p.parts = static_cast<uint32_t>(std::min<int64_t>((p.rows + p.groups - 1) / p.groups, p.parts));
+    if (p.cluster > 1) return launch_back<BF16, RES, 4, true>(p, st);
+    if (v == 1) return launch_back<BF16, RES, 1, false>(p, st);
+    if (v == 2) return launch_back<BF16, RES, 2, false>(p, st);
+    return launch_back<BF16, RES, 4, false>(p, st);
 }
 
 }  // namespace mxnorm
@@ -801,7 +858,7 @@ cudaError_t mx_launch_rmsnorm_backward(const MxNormBackArgs &a, cudaStream_t st)
     const cudaError_t e = a.xdt == MX_BF16 ? (p.dres ? launch_backward_v<true, true>(p, st) : launch_backward_v<true, false>(p, st))
                                            : (p.dres ? launch_backward_v<false, true>(p, st) : launch_backward_v<false, false>(p, st));
     if (e != cudaSuccess) return e;
-    return launch_early(norm_dweight_kernel, p.cols / 32, 32 * DW_WARPS, 0, st, static_cast<const float *>(p.part), p.parts,
+    return launch_early(norm_dweight_kernel, p.cols / 32, 1, 32 * DW_WARPS, 0, st, static_cast<const float *>(p.part), p.parts,
                         p.cols, p.dw);
 }
 

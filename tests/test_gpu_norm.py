@@ -278,6 +278,13 @@ def test_backward(rows, cols, dtype, res):
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
 
 
+@pytest.mark.parametrize("rows,cols", [(70, 8224), (150, 16416), (149, 20000), (80, 32768)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_backward_of_wide_rows(rows, cols, dtype):
+    """Rows that two or four CTAs share, in uneven pieces, and more rows than run at a time."""
+    test_backward(rows, cols, dtype, True)
+
+
 def test_backward_against_differences():
     """Directional derivatives of the forward formula in fp64.  With step t the
     central difference is off by t^2 / 6 times the third derivative; t = 1e-4
