@@ -26,6 +26,29 @@
 //    into the same sum.
 // The number of parts depends on N and K alone, and a token is a column of its
 // own, so a token's result does not depend on the other tokens.
+//
+// What bounds it.  The weights are read once, at 5.9 TB/s while they stream (a
+// copy makes 6.5): one token x 28672 x 4096 takes 15.1 us where their bytes take
+// 9.6.  The rest is what a call has before and after the stream: 2.3 us of launch
+// and first loads, 0.9 us of staging (2.6 for sixteen tokens, 2.2 for eight of
+// K = 14336), 0.5 us of adding the parts (2.4 in a cluster, for its barriers and
+// the slowest of its CTAs) and 1.3 us of products that do not hide behind copies
+// (2.1 with eight tokens, 3.4 with two tiles of tokens).  So 1 x 4096 x 4096
+// takes 5.5 us (bytes: 1.4), 8 x 4096 x 14336 13.4 and 16 x 14336 x 4096 16.1
+// (4.8), NVFP4 18.2 (5.1).  fp32 activations have three times the products: 27.7
+// us for 28672 x 4096.
+//
+// Measured against the choices here (us, one token x 28672 x 4096 where not said):
+//  - rings of three or four slices 17.7, two 16.9; a slot refilled behind its
+//    products, with two slices in flight, 15.9, before them, with one, 15.3: the
+//    activations' loads queue behind the weights'
+//  - rows copied in 64-byte pieces 16.9, whole slices by eight lanes 15.6
+//  - 16, 20, 26 warps to a CTA 18.0, 17.9, 16.2, 28 (all that 72 registers leave
+//    room for) 15.3; 28 also take 16 x 14336 x 4096 in four parts: 18.5 against 23.2
+//  - fp32 activations as three fp16 terms 25.7 against 28.0, but 4 x 9000 x 4112
+//    NVFP4 25.9 against 18.8 (K's tail mixes types), 3 x 1001 x 2080 8.2 against
+//    6.8, and bf16's 16.1 against 15.3 by registers
+//  - codes by matrix loads (ldmatrix) instead of words: the same, 15.0 and 15.1
 #include <algorithm>
 #include <cooperative_groups.h>
 #include <cstdint>
@@ -43,7 +66,7 @@ using namespace mxk;
 namespace cg = cooperative_groups;
 
 constexpr int ATOM = 128;            // weight rows of a scale atom: eight tiles
-constexpr int SLICE = 256;           // codes of a row per slice
+constexpr int SLICE = 256;           // codes of a row per slice: a 128-byte line
 constexpr int DEPTH = 2;             // slices in a warp's ring
 constexpr int PITCH = SLICE / 2 + 16;      // bytes of a row's slice in the ring: eight rows' words in different banks
 constexpr int MAX_WARPS = 28;
@@ -632,8 +655,15 @@ cudaError_t launch_kernel(GemvParams &p, int sms, cudaStream_t st) {
     // with the tiles spread over all SMs, a multiple of four (or eight) so that
     // they can be shared out over a cluster.
     const uint32_t most = ceil_div(p.tiles, sms);                  // tiles per SM
-    uint32_t idle = 1;                                             // SMs for each tile: a cluster's, if there are so many
-    while (idle < 8 && p.tiles <= max_clusters(kern, 2 * idle, sms)) idle *= 2;
+    // SMs for each tile: a cluster's if there are so many, and slices enough to
+    // make up for its barriers.  Measured (us, one SM to a tile and a cluster):
+    // one token x 1024 x 4096 (16 slices) bf16 4.0 and 4.4, fp32 5.6 and 5.1;
+    // 3 x 1001 x 2080 (9) 4.7 and 5.4, 6.5 and 6.6; 1 x 777 x 1056 (5) 3.4 and
+    // 4.3, 4.5 and 5.4; 3 x 777 x 5120 (20) 6.9 and 5.5, 9.2 and 6.7;
+    // 1 x 1024 x 14336 (56) 7.9 and 6.8, 12.5 and 10.1; 1 x 256 x 16384 (64)
+    // 7.5 and 6.4, 14.1 and 7.1.
+    uint32_t idle = 1;
+    while (p.slices > (XF32 ? 8 : 16) && idle < 8 && p.tiles <= max_clusters(kern, 2 * idle, sms)) idle *= 2;
     p.parts = 1;
     if (most <= MAX_WARPS / 2) {
         // with room for a step's activations of the most tokens that a CTA can have
@@ -724,6 +754,9 @@ cudaError_t mx_launch_gemv(const MxGemvArgs &a, cudaStream_t st) {
     p.tiles = p.n / ATOM * 8 + (rest >= 32 ? 8 : (rest + 3) / 4);
     p.alpha = a.alpha; p.y = a.y; p.y_f32 = a.ydt == MX_F32; p.ldy = a.ldy;
     const bool nv = a.enc != nullptr;
+    // Two tiles of tokens to a CTA from nine tokens on, as the registers allow with
+    // bf16 alone: 16 x 14336 x 4096 takes 16.1 us, with a tile to each of two CTAs
+    // (the weights read twice) 21.9.
     if (a.xdt == MX_F32) return nv ? launch<true, true, 1>(p, bytes, a.num_sms, st) : launch<true, false, 1>(p, bytes, a.num_sms, st);
     if (p.tokens <= 8) return nv ? launch<false, true, 1>(p, bytes, a.num_sms, st) : launch<false, false, 1>(p, bytes, a.num_sms, st);
     return nv ? launch<false, true, 2>(p, bytes, a.num_sms, st) : launch<false, false, 2>(p, bytes, a.num_sms, st);

@@ -321,9 +321,9 @@ __device__ __forceinline__ void cast_as(const NormParams &p, int64_t row, uint32
 // Vectors past the row's end are zero, like their weights, and not stored.
 // Memory bounds it: a bf16 row with a residual moves 4 bytes a value in, 2 of h
 // out, and 2 of y or 1 + 1/32 of E4M3 codes.  Measured (16384 x 4096 bf16):
-// 88 us, 6.1 TB/s, with y, and 83 us, 5.7 TB/s, with codes (a copy makes 6.5;
-// the cast's instructions fill half of the issue slots); 8192 x 4096 fp32 with
-// codes 73 us, 6.0 TB/s; one row of 4096 1.8 us, a chain of latencies.
+// 88 us, 6.1 TB/s, with y, and 83 us, 5.7 TB/s, with codes (a copy makes 6.5);
+// 8192 x 4096 fp32 with codes 73 us, 6.0 TB/s; one row of 4096 1.8 us, a chain
+// of latencies.
 template <bool BF16, bool RES, int V, int T, int CAST>
 __global__ void __launch_bounds__(T, 1) norm_kernel(const __grid_constant__ NormParams p) {
     // the next row's loads are in flight while this one is worked on, where registers allow
@@ -743,17 +743,19 @@ cudaError_t launch_norm_cast(const NormParams &p, int cast, int sms, cudaStream_
     }
 }
 
-// Vectors of a thread: few where a row has to be spread over many threads, more
-// where a wider CTA would only make the sum's barriers longer; 32 rows of a CTA's
-// threads are the most that keep several CTAs on an SM.  Measured (bf16 with
-// residual and E4M3 cast, us with V = 1, 2, 4):
-//   vecs   32   32768 x 256    11.0  16.1  24.4
-//   vecs  128   16384 x 1024   21.6  22.9  20.3
-//   vecs  132   1013 x 1056     4.8   5.4
-//   vecs  512   16384 x 4096   82    82    85
-//   vecs 1024   4096 x 8192          45.8  42.3
-// and fp32, vecs 512, 8192 x 4096: 76, 73, 76 to 82.  (vecs 64: not measured,
-// as between its neighbours.)
+// Vectors of a thread: a row stays in one warp while four vectors a thread hold
+// it (its sum then needs no barrier), and takes about 256 threads beyond that,
+// fp32 512 with two vectors (four take too many registers for the next row to
+// be in flight).  Measured (with residual and E4M3 cast, us with V = 1, 2, 4):
+//   vecs   32   32768 x 256  bf16   10.7  15.7  23.7
+//   vecs   64   16384 x 512  bf16   11.1   9.8  14.4
+//   vecs  128   16384 x 1024 bf16   21.2  22.2  19.9
+//   vecs  132   1013 x 1056  fp32    4.5   5.3   5.9
+//   vecs  256   16384 x 2048 bf16   42.2  43.9  44.0
+//   vecs  512   16384 x 4096 bf16   82.4  82.9  84.7
+//   vecs  512   8192 x 4096  fp32   78.2  73.5  90.3
+//   vecs 1024   8192 x 8192  bf16         86.6  83.7
+//   vecs 1024   8192 x 8192  fp32          148   179
 template <bool BF16, bool RES>
 cudaError_t launch_norm_v(const NormParams &p, int cast, int sms, cudaStream_t st) {
     const int v = p.vecs <= 32 ? 1 : p.vecs <= 64 ? 2 : p.vecs <= 128 ? 4 : p.vecs <= 256 ? 1 : p.vecs <= (BF16 ? 512 : 1024) ? 2 : 4;
