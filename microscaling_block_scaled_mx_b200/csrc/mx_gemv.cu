@@ -85,7 +85,7 @@ struct GemvParams {
     uint32_t k_blocks, k_groups, slices;
     uint32_t tiles;            // of 16 rows
     uint32_t lanes, parts;     // tiles of a cluster at a time, parts of K of a tile
-    uint32_t share;            // a CTA's parts: it has lanes x share warps
+    uint32_t share;            // a CTA's parts: lanes x share of its warps have a tile, others only stage
     uint32_t lanes_inv, share_inv;      // 2^32 over them, rounded up: quotients of small numbers
     uint32_t size_log;         // CTAs of a cluster: 2^size_log
     uint32_t each, extra;      // tiles of a cluster, one more of the first `extra`
@@ -329,8 +329,9 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
     const uint32_t g = lane >> 2, t = lane & 3u;
     const uint32_t win = p.window * p.share;                   // slices in a window
     const uint32_t pitch = S::token(win), plane = p.tile * pitch;
-    uint8_t *ring = smem + warp * S::RING;                     // this warp's
-    uint8_t *acts = smem + warps * S::RING;                    // [planes][tile][pitch]
+    const uint32_t workers = p.lanes * p.share;                // warps with a tile
+    uint8_t *ring = smem + warp * S::RING;                     // a worker's
+    uint8_t *acts = smem + workers * S::RING;                // [planes][tile][pitch]
     uint8_t *flags = acts + S::PLANES * plane;                 // [win][8 NT]: the token is in bf16
     const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
 
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
     // Step i of a pass is slice i * parts + part of tile pass * lanes + col; a
     // warp without a tile, or past the last slice, only waits with the others.
     uint32_t tile = tile_lo + col, slot = 0;
-    const uint32_t mine = tile < tile_hi ? (p.slices - part + p.parts - 1) / p.parts : 0u;    // parts <= slices
+    const uint32_t mine = tile < tile_hi && warp < workers ? (p.slices - part + p.parts - 1) / p.parts : 0u;    // parts <= slices
     if (mine) {
         set_tile(tile);
         issue(part, 0);
@@ -585,7 +586,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
     __syncwarp();
     float *sums = reinterpret_cast<float *>(ring);
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NT && warp < workers; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) sums[(8 * i + 2 * t + (j & 1)) * 16 + g + 8 * (j >> 1)] = acc[i][j];
     if (size > 1) cg::this_cluster().sync();
@@ -704,18 +705,26 @@ cudaError_t launch_kernel(GemvParams &p, int sms, cudaStream_t st) {
     p.lanes = ceil_div(each, p.passes);
     p.lanes_inv = p.lanes == 1 ? 0 : static_cast<uint32_t>(((1ull << 32) + p.lanes - 1) / p.lanes);
     p.share_inv = p.share == 1 ? 0 : static_cast<uint32_t>(((1ull << 32) + p.share - 1) / p.share);
-    const uint32_t warps = p.lanes * p.share;
+    const uint32_t workers = p.lanes * p.share;
     // as many steps' activations at a time as fit, in windows of about the same size
     uint32_t windows = 1;
-    for (p.window = p.steps; p.window > 1 && S::smem(warps, p.tile, p.window * p.share) > SMEM_MAX;
+    for (p.window = p.steps; p.window > 1 && S::smem(workers, p.tile, p.window * p.share) > SMEM_MAX;
          p.window = ceil_div(p.steps, windows))
         ++windows;
-    if (S::smem(warps, p.tile, p.window * p.share) > SMEM_MAX) return cudaErrorInvalidConfiguration;
+    if (S::smem(workers, p.tile, p.window * p.share) > SMEM_MAX) return cudaErrorInvalidConfiguration;
+
+    // Warps that stage a window in one batch of loads each: the CTA gets them if it
+    // has much fewer with a tile.  Measured (us, without and with): 8 x 777 x 1056
+    // (5 warps, 10 to stage) 6.7 and 4.5, 16 x 1024 x 4096 (8 and 32) 10.4 and 8.0,
+    // 3 x 1001 x 2080 fp32 (9 and 14) 6.6 and 5.7, but 8 x 4096 x 14336 (24 and 30)
+    // 13.5 and 13.8.
+    const uint32_t staff = ceil_div(p.tile * p.window * p.share, XF32 ? 2 : 4);
+    const uint32_t warps = 2 * staff >= 3 * workers ? std::max(workers, std::min(staff, uint32_t{MAX_WARPS})) : workers;
 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(clusters * size, ceil_div(p.tokens, 8 * NT));
     cfg.blockDim = dim3(32 * warps);
-    cfg.dynamicSmemBytes = S::smem(warps, p.tile, p.window * p.share);
+    cfg.dynamicSmemBytes = S::smem(workers, p.tile, p.window * p.share);
     cfg.stream = st;
     // Programmatic serialization: this kernel's CTAs may start before the stream's
     // last kernel has drained.  Back to back, one token x 28672 x 4096 takes 15.9 us
