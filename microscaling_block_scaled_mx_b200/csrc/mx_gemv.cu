@@ -28,14 +28,14 @@
 // own, so a token's result does not depend on the other tokens.
 //
 // What bounds it.  The weights are read once, at 5.9 TB/s while they stream (a
-// copy makes 6.5): one token x 28672 x 4096 takes 15.1 us where their bytes take
+// copy makes 6.5): one token x 28672 x 4096 takes 15.2 us where their bytes take
 // 9.6.  The rest is what a call has before and after the stream: 2.3 us of launch
 // and first loads, 0.9 us of staging (2.6 for sixteen tokens, 2.2 for eight of
 // K = 14336), 0.5 us of adding the parts (2.4 in a cluster, for its barriers and
 // the slowest of its CTAs) and 1.3 us of products that do not hide behind copies
 // (2.1 with eight tokens, 3.4 with two tiles of tokens).  So 1 x 4096 x 4096
-// takes 5.5 us (bytes: 1.4), 8 x 4096 x 14336 13.4 and 16 x 14336 x 4096 16.1
-// (4.8), NVFP4 18.2 (5.1).  fp32 activations have three times the products: 27.7
+// takes 5.5 us (bytes: 1.4), 8 x 4096 x 14336 13.5 and 16 x 14336 x 4096 16.2
+// (4.8), NVFP4 18.3 (5.1).  fp32 activations have three times the products: 27.5
 // us for 28672 x 4096.
 //
 // Measured against the choices here (us, one token x 28672 x 4096 where not said):
