@@ -429,3 +429,30 @@ def test_two_and_three_parts_of_k(N):
     w = np.empty((len(pick), K))
     w[:, 0::2], w[:, 1::2] = VALUES[c & 15], VALUES[c >> 4]
     check(y[:, pick], x, w * np.repeat(np.exp2(s.astype(np.float64) - 127), 32, axis=1))
+
+
+@pytest.mark.parametrize("M,N,K,dtype", [
+    (3, 1, 32, torch.float32), (3, 1, 512, torch.float32),                # one tile, warps that only stage
+    (3, 17, 2080, torch.float32), (3, 1, 65536, torch.float32),           # a cluster of eight, one and two windows
+    (16, 33, 4096, torch.bfloat16), (16, 1000, 8192, torch.bfloat16), (8, 777, 1056, torch.bfloat16),
+    (3, 300, 2080, torch.float32), (8, 300, 28672, torch.float32),        # a cluster of four
+    (8, 1000, 8192, torch.float32), (8, 2300, 2080, torch.float32), (8, 4100, 28672, torch.bfloat16),
+    (8, 20000, 2080, torch.float32), (8, 41000, 4096, torch.float32),     # whole rows to a warp, more passes than one
+    (3, 70000, 4096, torch.bfloat16), (30, 128, 131072, torch.bfloat16)])
+def test_forms_of_the_launch(M, N, K, dtype):
+    """Every way in which the work is cut over warps, clusters and windows: the
+    first and last token as when they come alone, rows against the product."""
+    g = torch.Generator(device=dev()).manual_seed(60)
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=dev(), generator=g)
+    scales = torch.randint(118, 130, (N, K // 32), dtype=torch.uint8, device=dev(), generator=g)
+    x = activations(M, K, dtype, 61)
+    x[M - 1, K // 2] = 3e4                          # a slice of the last token past fp16's range
+    y = mx.gemv(codes, scales, x, N, K, scale_layout="plain", out_dtype=torch.float32)
+    for i in (0, M - 1):
+        assert torch.equal(y[i:i + 1], mx.gemv(codes, scales, x[i:i + 1], N, K, scale_layout="plain",
+                                               out_dtype=torch.float32))
+    pick = sorted({0, 1 % N, N // 3, N // 2, max(N - 17, 0), N - 1})
+    c, s = codes[pick].cpu().numpy(), scales[pick].cpu().numpy()
+    w = np.empty((len(pick), K))
+    w[:, 0::2], w[:, 1::2] = VALUES[c & 15], VALUES[c >> 4]
+    check(y[:, pick], x, w * np.repeat(np.exp2(s.astype(np.float64) - 127), 32, axis=1))

@@ -285,6 +285,36 @@ def test_backward_of_wide_rows(rows, cols, dtype):
     test_backward(rows, cols, dtype, True)
 
 
+@pytest.mark.parametrize("cols", [4096, 20000])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_backward_in_place_on_a_stream_and_captured(cols, dtype):
+    """dx over dy and over dres, off the current stream and in a graph: the same bits."""
+    rows = 300
+    h, w, dy, dres, rstd = back_inputs(rows, cols, dtype, 31, True)
+    dx, dw = mx.rmsnorm_backward(dy, h, w, rstd, dres=dres)
+    for place in (dy, dres):
+        copies = dy.clone(), dres.clone()
+        into = copies[0] if place is dy else copies[1]
+        ws = mx.rmsnorm_backward_workspace(rows, cols)
+        got_w = torch.empty_like(dw)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        mx.rmsnorm_backward(copies[0], h, w, rstd, dres=copies[1], out=(into, got_w), workspace=ws, stream=s)
+        s.synchronize()
+        assert torch.equal(into, dx) and torch.equal(got_w, dw)
+    out = torch.empty_like(dx), torch.empty_like(dw)
+    ws = mx.rmsnorm_backward_workspace(rows, cols)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):                          # one after the other in the same workspace
+            mx.rmsnorm_backward(dy, h, w, rstd, dres=dres, out=out, workspace=ws)
+    for t in (*out, ws):
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], dx) and torch.equal(out[1], dw)
+
+
 def test_backward_against_differences():
     """Directional derivatives of the forward formula in fp64.  With step t the
     central difference is off by t^2 / 6 times the third derivative; t = 1e-4
