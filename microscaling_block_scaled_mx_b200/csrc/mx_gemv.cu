@@ -8,12 +8,12 @@
 // a tile where there are fewer tiles than warps.  The parts of a tile are spread
 // over its cluster's CTAs, so that each stages the activations of its parts
 // alone, and their sums are added in order through (distributed) shared memory.
-// A warp walks along its K in slices of 256 codes, 128 bytes
-// of each row, copied asynchronously into its own ring, so that warps wait for
-// one another only where activations are staged.  It multiplies its 16 rows
-// with eight tokens at a time by m16n8k16 tensor-core products with fp32 sums,
-// a 32-code chunk per pair of products; the chunk's sum times its scale is
-// added to the running sum in fp32.  All operands of the products are exact:
+// A warp walks along its K in slices of 256 codes, 128 bytes of each row, copied
+// asynchronously into its own ring, so that warps wait for one another only
+// where activations are staged.  It multiplies its 16 rows with eight tokens at
+// a time by m16n8k16 tensor-core products with fp32 sums, a 32-code chunk per
+// pair of products; the chunk's sum times its scale is added to the running sum
+// in fp32.  All operands of the products are exact:
 //  - E2M1 codes become fp16 by the hardware conversion, two per instruction.
 //    NVFP4's E4M3 scale multiplies them there: a code times a scale is a
 //    multiple of 2^-10 up to 2688 with six significant bits.
@@ -24,8 +24,9 @@
 //  - fp32 activations are split into three bf16 terms (8 + 8 + 8 bits, by
 //    truncation, exact down to bf16's smallest subnormal) whose products go
 //    into the same sum.
-// The number of parts depends on N and K alone, and a token is a column of its
-// own, so a token's result does not depend on the other tokens.
+// The number of parts depends on N, K, the device and the activations' type, and
+// a token is a column of its own, so a token's result does not depend on the
+// other tokens.
 //
 // What bounds it.  The weights are read once, at 5.9 TB/s while they stream (a
 // copy makes 6.5): one token x 28672 x 4096 takes 15.2 us where their bytes take
