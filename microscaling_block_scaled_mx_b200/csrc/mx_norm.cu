@@ -798,6 +798,12 @@ cudaError_t launch_back(const BackParams &p, cudaStream_t st) {
 // CTA: 8192 x 4096 59 us against 49).  Where the SM has one CTA at a time, more
 // than 148 parts would run one after the other (2048 x 16384 65 us against 54);
 // of clusters the device may hold somewhat fewer than 148 CTAs' worth.
+// The parts decide dweight's bits, so they go by the three arrays that a row has
+// with dres, also without it.  Where two rows of two arrays would still fit into
+// half of the shared memory, the ring then has three (without dres, us with 296
+// parts and two rows, 148 and two, three, four): 8192 x 10240 bf16 104.7, 97.2,
+// 96.2, 98.1; 8192 x 5120 fp32 89.2, 85.8, 80.1, 80.3; 600 x 5120 fp32 15.9, 13.3,
+// 12.9, 14.1; 4096 x 7168 fp32 62.2, 58.0, 61.2, 61.0.
 template <bool BF16, bool RES>
 cudaError_t launch_backward_v(BackParams &p, cudaStream_t st) {
     p.cluster = p.pieces <= BACK_V * BACK_THREADS ? 1 : p.pieces <= 2 * BACK_V * BACK_THREADS ? 2 : 4;    // cols <= 32768
@@ -805,10 +811,11 @@ cudaError_t launch_backward_v(BackParams &p, cudaStream_t st) {
     const int v = p.pieces <= 32 ? 1 : p.pieces <= 384 || p.pieces > 512 ? 4 : 2;
     p.threads = threads_for(p.each, v);
     p.groups = std::max(1u, 256 / p.threads);
-    const int row = p.groups * (RES ? 3 : 2) * v * p.threads * 16;       // bytes of a stage, 96 KB at most
-    p.stages = std::max(2, std::min(4, BACK_HALF / row));
+    const int array = p.groups * v * p.threads * 16, row = (RES ? 3 : 2) * array;     // bytes of a stage, 96 KB at most
+    const bool one = 2 * 3 * array > BACK_HALF;                                     // CTA to an SM
+    p.stages = one && 2 * row <= BACK_HALF ? 3 : std::max(2, std::min(4, BACK_HALF / row));
     if (p.cluster > 1) p.parts = std::min(p.parts, p.cluster == 2 ? 72u : 32u);
-    else if (p.stages * row > BACK_HALF) p.parts = std::min(p.parts, 148u);
+    else if (one) p.parts = std::min(p.parts, 148u);
     p.parts = static_cast<uint32_t>(std::min<int64_t>((p.rows + p.groups - 1) / p.groups, p.parts));
     if (p.cluster > 1) return launch_back<BF16, RES, 4, true>(p, st);
     if (v == 1) return launch_back<BF16, RES, 1, false>(p, st);
