@@ -364,8 +364,11 @@ _NORM_RECORD = struct.Struct("=Q4qQqQqd3qQQqQqQQQqQ").pack
 _BACKWARD_RECORD = struct.Struct("=Q4qQqQqQQqQqQQqQ").pack
 _GEMV_RECORD = struct.Struct("=QQqqQqqQ5qdQqqQ").pack
 
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# torch's helpers behind torch.cuda.current_device and current_stream, which make
+# no wrapper objects; a torch without them (a CPU build) has the public functions.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda device: torch.cuda.current_stream(device).cuda_stream))
 
 
 def _device(t: torch.Tensor, what: str) -> int:
