@@ -620,15 +620,32 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, 1) gemv_kernel(const __grid_co
 
 uint32_t ceil_div(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
 
-// Clusters of `size` CTAs with all the shared memory that the device runs at a
-// time; asked once for each device.
-template <typename Kern>
-uint32_t max_clusters(Kern kern, int size, int sms) {
-    static std::atomic<uint32_t> known[64][4];
-    int dev = 0, n = 0, log = size == 2 ? 1 : size == 4 ? 2 : 3;
-    if (size == 1) return sms;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (const uint32_t k = known[dev][log].load(std::memory_order_relaxed)) return k;
+template <bool XF32, bool NV, int NT, bool BYTES>
+cudaError_t allow_smem() {
+    static std::atomic<uint64_t> done{0};
+    return ensure_smem_limit(gemv_kernel<XF32, NV, NT, BYTES>, SMEM_MAX, done);
+}
+
+// n = clusters of `size` CTAs with all the shared memory that the device runs at
+// a time; asked once for each device and size.  The parts of K follow from it,
+// so it is asked of one kernel for all (they have the same bounds): a token's
+// bits depend neither on its kernel, that is on how many tokens there are, nor
+// on which call came first.
+cudaError_t max_clusters(uint32_t size, int sms, uint32_t &n) {
+    static std::atomic<uint32_t> known[64][4];                     // the answer + 1
+    n = static_cast<uint32_t>(sms);
+    if (size == 1) return cudaSuccess;
+    int dev = 0, count = 0;
+    const int log = size == 2 ? 1 : size == 4 ? 2 : 3;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (const uint32_t k = known[dev][log].load(std::memory_order_relaxed)) {
+        n = k - 1;
+        return cudaSuccess;
+    }
+    e = allow_smem<false, false, 1, false>();
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(size);
     cfg.blockDim = dim3(32 * MAX_WARPS);
@@ -639,17 +656,18 @@ uint32_t max_clusters(Kern kern, int size, int sms) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) return 0;
-    known[dev][log].store(n, std::memory_order_relaxed);
-    return n;
+    e = cudaOccupancyMaxActiveClusters(&count, gemv_kernel<false, false, 1, false>, &cfg);
+    if (e != cudaSuccess) return e;
+    n = count > 0 ? static_cast<uint32_t>(count) : 0u;
+    known[dev][log].store(n + 1, std::memory_order_relaxed);
+    return cudaSuccess;
 }
 
 template <bool XF32, bool NV, int NT, bool BYTES>
 cudaError_t launch_kernel(GemvParams &p, int sms, cudaStream_t st) {
     using S = Shape<XF32, NV, NT>;
-    static std::atomic<uint64_t> done{0};
     auto kern = gemv_kernel<XF32, NV, NT, BYTES>;
-    cudaError_t e = ensure_smem_limit(kern, SMEM_MAX, done);
+    cudaError_t e = allow_smem<XF32, NV, NT, BYTES>();
     if (e != cudaSuccess) return e;
     p.tile = p.tokens < 8 * NT ? p.tokens : 8 * NT;
 
@@ -665,7 +683,13 @@ cudaError_t launch_kernel(GemvParams &p, int sms, cudaStream_t st) {
     // 1 x 1024 x 14336 (56) 7.9 and 6.8, 12.5 and 10.1; 1 x 256 x 16384 (64)
     // 7.5 and 6.4, 14.1 and 7.1.
     uint32_t idle = 1;
-    while (p.slices > (XF32 ? 8 : 16) && idle < 8 && p.tiles <= max_clusters(kern, 2 * idle, sms)) idle *= 2;
+    while (p.slices > (XF32 ? 8 : 16) && idle < 8) {
+        uint32_t n;
+        e = max_clusters(2 * idle, sms, n);
+        if (e != cudaSuccess) return e;
+        if (p.tiles > n) break;
+        idle *= 2;
+    }
     p.parts = 1;
     if (most <= MAX_WARPS / 2) {
         // with room for a step's activations of the most tokens that a CTA can have
@@ -688,11 +712,14 @@ cudaError_t launch_kernel(GemvParams &p, int sms, cudaStream_t st) {
     // 7.9 (16).
     uint32_t size = 0, clusters = 1;
     for (uint32_t c = 1; c <= 8 && p.parts % c == 0; c *= 2) {
-        const uint32_t n = std::min(p.tiles, max_clusters(kern, c, sms));
+        if (size >= idle && p.tile * p.slices <= 128 * size) break;
+        uint32_t n;
+        e = max_clusters(c, sms, n);
+        if (e != cudaSuccess) return e;
+        n = std::min(p.tiles, n);
         if (n == 0) continue;
         const uint32_t w = ceil_div(p.tiles, n) * (p.parts / c);
         if (p.parts > 1 && (w > MAX_WARPS || S::smem(w, p.tile, p.parts / c) > SMEM_MAX)) continue;
-        if (size >= idle && p.tile * p.slices <= 128 * size) break;
         size = c;
         clusters = n;
     }
