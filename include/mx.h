@@ -516,9 +516,12 @@ MX_API size_t mx_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
  *           gives zeros.  M at most 65536, N at most 2^31 - 1, K at most 2^24,
  *           scales below 4 GiB (MX_ERR_UNSUPPORTED).  Any M is right; mx_gemm
  *           is the faster call from a few dozen tokens on.
- * fp32 activations count down to 2^-133 (the bits below are dropped).  A NaN
- * scale makes its block's products NaN; NaN and Inf in x go by IEEE
- * rules (0 * Inf is NaN).
+ * fp32 activations count down to 2^-133 (the bits below are dropped).  A sum
+ * that passes fp32's range before its scale is Inf or NaN, also where the scaled
+ * result would fit: MXFP4's blocks of 32 products stay inside it for |x| up to
+ * 2^120, NVFP4's rows, whose scale by E comes last, for |x| up to 2^116 / K.
+ * A NaN scale makes its block's products NaN; NaN and Inf in x go by IEEE rules
+ * (0 * Inf is NaN).
  * Errors: MX_ERR_ARG, MX_ERR_ALIGN, MX_ERR_SHAPE, MX_ERR_UNSUPPORTED,
  * MX_ERR_CUDA.
  */
