@@ -512,7 +512,7 @@ namespace {
 constexpr int64_t kNormMaxCols = 32768;
 constexpr int64_t kMaxGrid = 2147483647;
 
-// CTAs of the backward pass, each with one row of partial sums of dweight:
+// At most so many CTAs in the backward pass, each with a row of dweight's partial sums:
 // two for each of the 148 SMs, whatever the device, so that the workspace's
 // size and the order of the sums depend on the sizes alone.
 int64_t norm_parts(int64_t rows) { return rows < 296 ? rows : 296; }
@@ -626,8 +626,6 @@ int mx_rmsnorm_backward(const void *dy, mx_dtype xdt, int64_t rows, int64_t cols
     a.dy = dy; a.h = h; a.dres = dres; a.xdt = xdt; a.rows = rows; a.cols = cols;
     a.lddy = lddy; a.ldh = ldh; a.lddres = lddres; a.lddx = lddx; a.weight = weight; a.wdt = wdt; a.rstd = rstd;
     a.dx = dx; a.dweight = dweight; a.part = static_cast<float *>(workspace); a.parts = norm_parts(rows);
-    a.num_sms = sm_count(nullptr);
-    if (a.num_sms <= 0) return MX_ERR_CUDA;
     return mx_launch_rmsnorm_backward(a, st) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
 }
 

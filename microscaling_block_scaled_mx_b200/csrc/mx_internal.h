@@ -116,7 +116,6 @@ struct MxNormBackArgs {
     void *dx;
     float *dweight, *part;         // part: parts x cols partial sums
     int64_t parts;
-    int num_sms;
 };
 
 struct MxGemvArgs {
