@@ -46,3 +46,28 @@ def test_plain_scales_at_an_odd_address(M, N, K, dtype, at):
     check(want, x, w)
     got = mx.gemv_nvfp4((codes, off_the_word(scales, at), enc), x, N, K, domain_rows=32, scale_layout="plain")
     assert torch.equal(got, want)
+
+
+def test_a_batch_of_thousands():
+    """More tokens than a wave of CTAs takes; each has the bits that it has alone."""
+    M, N, K = 4099, 77, 352
+    codes, scales, w = mx_weights(N, K, "mma", 6)
+    ws, w_nv = nv_weights(N, K, "mma", 7, 7)
+    for dtype in (torch.bfloat16, torch.float32):
+        x = activations(M, K, dtype, 8)
+        y, y_nv = mx.gemv(codes, scales, x, N, K), mx.gemv_nvfp4(ws, x, N, K, 7)
+        check(y, x, w)
+        check(y_nv, x, w_nv)
+        for i in (0, 2048, 4098):
+            assert torch.equal(mx.gemv(codes, scales, x[i:i + 1], N, K), y[i:i + 1])
+            assert torch.equal(mx.gemv_nvfp4(ws, x[i:i + 1], N, K, 7), y_nv[i:i + 1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_longest_rows(dtype):
+    M, N, K = 2, 3, 1 << 24
+    codes, scales, w = mx_weights(N, K, "plain", 9)
+    x = activations(M, K, dtype, 10)
+    y = mx.gemv(codes, scales, x, N, K, scale_layout="plain", out_dtype=torch.float32)
+    check(y, x, w)
+    assert torch.equal(mx.gemv(codes, scales, x[1:], N, K, scale_layout="plain", out_dtype=torch.float32), y[1:])
