@@ -496,9 +496,9 @@ MX_API size_t mx_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
  * for each handful of tokens, and four bits of it).  The weights' buffers are
  * those of mx_gemm's and mx_gemm_nvfp4's B operand, so that one copy of the
  * weights serves both.  Products with the codes are exact, sums are fp32 in an
- * order fixed by N, K and the types, whatever the other tokens are and however
- * many; the scales multiply fp32 partial sums (MXFP4) or the codes, exactly
- * (NVFP4).  The sum is multiplied by alpha (NVFP4: fl32(alpha / E) of its row's
+ * order fixed by N, K, the types and the device, whatever the other tokens are
+ * and however many; the scales multiply fp32 partial sums (MXFP4) or the codes,
+ * exactly (NVFP4).  The sum is multiplied by alpha (NVFP4: fl32(alpha / E) of its row's
  * domain) in fp32 and rounded to ydt.
  *
  *  w_codes  device, N x K codes (K / 2 bytes per row), 16-byte aligned.

@@ -44,8 +44,13 @@
 //    products, with two slices in flight, 15.9, before them, with one, 15.3: the
 //    activations' loads queue behind the weights'
 //  - rows copied in 64-byte pieces 16.9, whole slices by eight lanes 15.6
-//  - 16, 20, 26 warps to a CTA 18.0, 17.9, 16.2, 28 (all that 72 registers leave
-//    room for) 15.3; 28 also take 16 x 14336 x 4096 in four parts: 18.5 against 23.2
+//  - at most 16, 20, 24, 26 and 28 warps to a CTA: 17.0, 17.2, 17.6, 15.4, 15.4 (13
+//    have a tile, and 26 where two parts of K fit); 16 x 14336 x 4096 (2, 2, 3, 3 and
+//    4 parts, a cluster's where they are even) 16.9, 16.6, 19.9, 21.2, 16.6, NVFP4
+//    18.6, 18.2, 21.6, 23.6, 18.7; 16 x 4096 x 4096 9.7, 9.8, 10.1, 10.4, 10.5;
+//    8 x 4096 x 14336 13.0, 13.5, 14.0, 14.0, 14.0.  28 is what 72 registers leave
+//    room for; the kernels of two tiles of tokens spill 48 to 108 bytes a thread
+//    there and 8 to 44 at 20 warps and 96 registers, the others up to 52
 //  - fp32 activations as three fp16 terms 25.7 against 28.0, but 4 x 9000 x 4112
 //    NVFP4 25.9 against 18.8 (K's tail mixes types), 3 x 1001 x 2080 8.2 against
 //    6.8, and bf16's 16.1 against 15.3 by registers
@@ -673,7 +678,10 @@ cudaError_t launch_kernel(GemvParams &p, int sms, cudaStream_t st) {
 
     // Parts of K, from N, K and the device alone: as many as there are warps for
     // with the tiles spread over all SMs, a multiple of four (or eight) so that
-    // they can be shared out over a cluster.
+    // they can be shared out over a cluster.  That rounding leaves warps without a
+    // tile at some widths, also where no cluster shares them: 1 x 5120 x 5120 has 4
+    // parts of the 9 that fit, 12 warps, 7.4 us (bytes: 2.1); 8192 x 8192 4 of 7, 16
+    // warps, 11.6 us (5.5); 11008 x 4096 4 of 5, 20 warps, 8.8 us (3.7).
     const uint32_t most = ceil_div(p.tiles, sms);                  // tiles per SM
     // SMs for each tile: a cluster's if there are so many, and slices enough to
     // make up for its barriers.  Measured (us, one SM to a tile and a cluster):

@@ -323,7 +323,9 @@ __device__ __forceinline__ void cast_as(const NormParams &p, int64_t row, uint32
 // out, and 2 of y or 1 + 1/32 of E4M3 codes.  Measured (16384 x 4096 bf16):
 // 88 us, 6.1 TB/s, with y, and 83 us, 5.7 TB/s, with codes (a copy makes 6.5);
 // 8192 x 4096 fp32 with codes 73 us, 6.0 TB/s; one row of 4096 1.8 us, a chain
-// of latencies.
+// of latencies.  Other casts of 16384 x 4096 bf16 (us; a copy of their bytes 67 to
+// 72): E2M1 77, E2M3 82, E3M2 82, INT8 92; stochastic rounding E4M3 85, E2M1 88,
+// E2M3 90, INT8 111.
 template <bool BF16, bool RES, int V, int T, int CAST>
 __global__ void __launch_bounds__(T, 1) norm_kernel(const __grid_constant__ NormParams p) {
     // the next row's loads are in flight while this one is worked on, where registers allow
@@ -756,6 +758,11 @@ cudaError_t launch_norm_cast(const NormParams &p, int cast, int sms, cudaStream_
 //   vecs  512   8192 x 4096  fp32   78.2  73.5  90.3
 //   vecs 1024   8192 x 8192  bf16         86.6  83.7
 //   vecs 1024   8192 x 8192  fp32          148   179
+// Wider rows have four vectors a thread: fp32 without the next row in flight and
+// with one CTA to an SM (108 registers x 512 threads), 4096 x 16384 183, 4.8 TB/s
+// (with y instead of codes 196, 5.5); bf16 in the same way beyond 512 threads, 2048 x
+// 32768 88, 5.4 TB/s (91, 5.9).  At 1024 threads fp32 with a residual spills up to
+// 40 bytes of its 64 registers.
 template <bool BF16, bool RES>
 cudaError_t launch_norm_v(const NormParams &p, int cast, int sms, cudaStream_t st) {
     const int v = p.vecs <= 32 ? 1 : p.vecs <= 64 ? 2 : p.vecs <= 128 ? 4 : p.vecs <= 256 ? 1 : p.vecs <= (BF16 ? 512 : 1024) ? 2 : 4;
